@@ -64,6 +64,21 @@ class GdnAttnLayer(ctypes.Structure):
     ]
 
 
+ROPE_MAX_HEAD_DIM = 256
+MAX_TREE_NODES = 64
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class GdnRope(ctypes.Structure):
+    """gdn_rope: the table of one rotary embedding (filled by gdn_rope_init, then only read)."""
+    _fields_ = [
+        ("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+        ("eps", ctypes.c_float), ("amplitude", ctypes.c_float),
+        ("turns", ctypes.c_ulonglong * (ROPE_MAX_HEAD_DIM // 2)),
+    ]
+
+
 ATTN_Q_HEADS, ATTN_KV_HEADS, ATTN_HEAD_DIM = 24, 4, 256
 ATTN_N_IN = 2 * 24 * 256 + 2 * 4 * 256
 
@@ -75,6 +90,7 @@ SCHEDULE_FUSED = 2         # one overlapped launch whenever the scan units fit i
 
 _lib = None
 _vp, _sz, _i, _ll = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_longlong
+_f, _d = ctypes.c_float, ctypes.c_double
 
 EXPORTS = ("gdn_prefill_workspace_size", "gdn_prefill", "gdn_prefill_varlen", "gdn_prefill_host_workspace_size",
            "gdn_prefill_host", "gdn_decode_step",
@@ -82,7 +98,11 @@ EXPORTS = ("gdn_prefill_workspace_size", "gdn_prefill", "gdn_prefill_varlen", "g
            "gdn_layer_decode_workspace_size", "gdn_layer_decode",
            "gdn_attn_layer_workspace_size", "gdn_attn_layer_prefill", "gdn_attention_prefill",
            "gdn_attn_decode_workspace_size", "gdn_attn_layer_decode_step", "gdn_status_string",
-           "gdn_err_status", "gdn_prefill_fused_plan")
+           "gdn_err_status", "gdn_prefill_fused_plan",
+           "gdn_decode_tree", "gdn_decode_tree_commit", "gdn_layer_tree_workspace_size", "gdn_layer_decode_tree",
+           "gdn_layer_tree_commit", "gdn_rope_init", "gdn_qk_norm_rope", "gdn_attention_tree_workspace_size",
+           "gdn_attention_tree", "gdn_attn_tree_commit", "gdn_attn_layer_tree_workspace_size",
+           "gdn_attn_layer_decode_tree", "gdn_attn_layer_tree_commit")
 MAX_DECODE_TOKENS = 8
 
 
@@ -144,6 +164,31 @@ def load(path: str | None = None, fresh: bool = False):
     lib.gdn_err_status.restype = _i
     lib.gdn_prefill_fused_plan.argtypes = [_i, _i, _i, _ll, _i, _i]
     lib.gdn_prefill_fused_plan.restype = _i
+    lib.gdn_decode_tree.argtypes = [P, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp]
+    lib.gdn_decode_tree_commit.argtypes = [P, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp]
+    lib.gdn_layer_tree_workspace_size.argtypes = [_i, _i, _i, _i]
+    lib.gdn_layer_decode_tree.argtypes = [ctypes.POINTER(GdnLayer), _i, _i, _vp, _vp, _ll, _vp, _vp, _vp, _i, _vp, _ll,
+                                          _vp, _sz, _vp, _vp]
+    lib.gdn_layer_tree_commit.argtypes = [ctypes.POINTER(GdnLayer), _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp,
+                                          _vp]
+    lib.gdn_rope_init.argtypes = [ctypes.POINTER(GdnRope), _i, _i, _i, _i, _d, _d, _i, _d, _d, _f]
+    lib.gdn_qk_norm_rope.argtypes = [ctypes.POINTER(GdnRope), _ll, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp,
+                                     _vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp]
+    lib.gdn_attention_tree_workspace_size.argtypes = [_i, _i, _i, _i, _i]
+    lib.gdn_attention_tree.argtypes = [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _i, _vp, _vp, _vp, _ll, _i, _i, _i, _f, _i,
+                                       _i, _vp, _vp, _sz, _vp, _vp]
+    lib.gdn_attn_tree_commit.argtypes = [_vp, _ll, _vp, _ll, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp]
+    lib.gdn_attn_layer_tree_workspace_size.argtypes = [_i, _i]
+    lib.gdn_attn_layer_decode_tree.argtypes = [ctypes.POINTER(GdnAttnLayer), _i, _i, _vp, _vp, _ll, _vp, _vp, _i, _vp,
+                                               _vp, _ll, _vp, _sz, _vp, _vp]
+    lib.gdn_attn_layer_tree_commit.argtypes = [_i, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _sz, _vp, _vp]
+    for name in ("gdn_decode_tree", "gdn_decode_tree_commit", "gdn_layer_decode_tree", "gdn_layer_tree_commit",
+                 "gdn_rope_init", "gdn_qk_norm_rope", "gdn_attention_tree", "gdn_attn_tree_commit",
+                 "gdn_attn_layer_decode_tree", "gdn_attn_layer_tree_commit"):
+        getattr(lib, name).restype = _i
+    for name in ("gdn_layer_tree_workspace_size", "gdn_attention_tree_workspace_size",
+                 "gdn_attn_layer_tree_workspace_size"):
+        getattr(lib, name).restype = _sz
     if not fresh:
         _lib = lib
     return lib
@@ -441,6 +486,271 @@ def attention_prefill(q_hat, k, v, g, B: int, T: int, out=None, err=None):
     _check(lib.gdn_attention_prefill(_ptr(q_hat), _ptr(k), _ptr(v), _ptr(g2), g2.stride(0), B, T, _ptr(out),
                                      _ptr(err), _stream()), "gdn_attention_prefill")
     return out
+
+
+# ------------------------------------------------------------------ trees of drafted tokens
+
+def _run_on(device, name, *args):
+    """Call entry point `name` on `device` and its current stream (which comes last)."""
+    with torch.cuda.device(device):
+        _check(getattr(load(), name)(*args, _stream()), name)
+
+
+def _want(name, t, dtype, shape=None, device=None):
+    """A contiguous tensor of this type (and shape) on this device, or None."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _heads(name, t, device=None):
+    """(heads, head_dim, token stride) of a bf16 [tokens][heads][head_dim] tensor, its rows contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bf16, not {t.dtype}")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [tokens][heads][head_dim] with contiguous rows")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.shape[1], t.shape[2], (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2]))
+
+
+def _want_pool(H_k, H_v, state, conv_state, what=""):
+    slots, dev = state.shape[0], state.device
+    _want("state" + what, state, torch.float32, (slots, H_v, HEAD_DIM, HEAD_DIM), dev)
+    _want("conv_state" + what, conv_state, torch.bfloat16, (slots, 3, (2 * H_k + H_v) * HEAD_DIM), dev)
+    return slots, dev
+
+
+def decode_tree(inp: GdnInputs, N: int, T: int, parent, state, conv_state, state_slot=None, out=None, err=None):
+    """gdn_decode_tree: the outputs of T tree nodes per sequence (node n*T + t), each after its own path.
+
+    parent: device int32 [N][T] (-1 a child of the last committed token, an earlier node, or -2 for no
+    node), None for a chain.  state and conv_state (the pools) are read.  Returns out [N*T][H_v][128] bf16."""
+    slots, dev = _want_pool(inp.H_k, inp.H_v, state, conv_state)
+    _want("parent", parent, torch.int32, (N, T), dev)
+    _want("state_slot", state_slot, torch.int32, (N,), dev)
+    if out is None:
+        out = torch.empty(N * T, inp.H_v, HEAD_DIM, dtype=torch.bfloat16, device=dev)
+    _want("out", out, torch.bfloat16, (N * T, inp.H_v, HEAD_DIM), dev)
+    _run_on(dev, "gdn_decode_tree", ctypes.byref(inp), N, T, _ptr(parent), _ptr(state), _ptr(conv_state),
+            _ptr(state_slot), slots, _ptr(out), _ptr(err))
+    return out
+
+
+def decode_tree_commit(inp: GdnInputs, N: int, T: int, parent, accepted, state, conv_state, state_slot=None, *,
+                       state_out=None, conv_out=None, err=None):
+    """gdn_decode_tree_commit: state and conv_state advanced along each sequence's path to node accepted[n]
+    (device int32 [N], -1: none), in place unless state_out / conv_out are given.  Returns both."""
+    slots, dev = _want_pool(inp.H_k, inp.H_v, state, conv_state)
+    state_out = state if state_out is None else state_out
+    conv_out = conv_state if conv_out is None else conv_out
+    if _want_pool(inp.H_k, inp.H_v, state_out, conv_out, "_out") != (slots, dev):
+        raise ValueError("state_out must have the slots of state, on its device")
+    _want("parent", parent, torch.int32, (N, T), dev)
+    _want("accepted", accepted, torch.int32, (N,), dev)
+    _want("state_slot", state_slot, torch.int32, (N,), dev)
+    _run_on(dev, "gdn_decode_tree_commit", ctypes.byref(inp), N, T, _ptr(parent), _ptr(accepted), _ptr(state),
+            _ptr(state_out), _ptr(conv_state), _ptr(conv_out), _ptr(state_slot), slots, _ptr(err))
+    return state_out, conv_out
+
+
+def make_rope(head_dim: int, rotary_dim: int | None = None, *, base: float = 1e7, interleaved: bool = False,
+              scaling: str = "none", factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0,
+              beta_slow: float = 1.0, eps: float = 1e-6) -> GdnRope:
+    """gdn_rope_init: the table of a rotary embedding on the first rotary_dim dims of each head (default all),
+    scaling "none", "linear", "ntk" or "yarn"; eps is the norms'.  Made once and kept."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, not {scaling!r}")
+    rope = GdnRope()
+    _check(load().gdn_rope_init(ctypes.byref(rope), head_dim, head_dim if rotary_dim is None else rotary_dim,
+                                ROPE_INTERLEAVED if interleaved else ROPE_HALF, ROPE_SCALINGS[scaling], base, factor,
+                                original_len, beta_fast, beta_slow, eps), "gdn_rope_init")
+    return rope
+
+
+def qk_norm_rope(rope: GdnRope, q, k=None, v=None, *, q_norm_w=None, k_norm_w=None, positions=None, rows=None,
+                 q_out=None, k_out=None, v_out=None, err=None):
+    """gdn_qk_norm_rope on q [tokens][H_q][D] and k, v [tokens][H_kv][D] (token-strided views are fine; q or k
+    may be None): norm per head (None weights: no norm), rotation by positions (device int32, None: 0, 1, ..),
+    k and v stored at `rows` (device int64, negative: not stored) of k_out, v_out [n_rows][H_kv][D].
+    Returns (q_out, k_out, v_out)."""
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("q or k is needed")
+    dev, n_tok, D = lead.device, lead.shape[0], rope.head_dim
+    H_q = H_kv = 0
+    ld = dict.fromkeys(("q", "k", "v", "q_out", "k_out", "v_out"), 0)
+    if v is not None and k is None:
+        raise ValueError("v needs k")
+    if rows is not None and k is not None and (k_out is None or (v is not None and v_out is None)):
+        raise ValueError("rows needs k_out and v_out")
+    if q is not None and q_out is None:
+        q_out = torch.empty(n_tok, q.shape[1], D, dtype=torch.bfloat16, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty(n_tok, k.shape[1], D, dtype=torch.bfloat16, device=dev)
+    if v is not None and v_out is None:
+        v_out = torch.empty(n_tok, v.shape[1], D, dtype=torch.bfloat16, device=dev)
+    for name, t in (("q", q), ("q_out", q_out if q is not None else None)):
+        if t is not None:
+            H_q, d, ld[name] = _heads(name, t, dev)
+            if d != D or t.shape[0] != n_tok or H_q != q.shape[1]:
+                raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
+    for name, t in (("k", k), ("v", v), ("k_out", k_out if k is not None else None),
+                    ("v_out", v_out if v is not None else None)):
+        if t is not None:
+            H_kv, d, ld[name] = _heads(name, t, dev)
+            if d != D or H_kv != k.shape[1] or (name in ("k", "v") and t.shape[0] != n_tok):
+                raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
+    n_rows = k_out.shape[0] if k is not None else 0
+    if v is not None and v_out.shape[0] != n_rows:
+        raise ValueError("k_out and v_out must have the same rows")
+    for name, t in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w)):
+        _want(name, t, torch.bfloat16, (D,), dev)
+    _want("positions", positions, torch.int32, (n_tok,), dev)
+    _want("rows", rows, torch.int64, (n_tok,), dev)
+    _run_on(dev, "gdn_qk_norm_rope", ctypes.byref(rope), n_tok, H_q, H_kv, _ptr(q), ld["q"], _ptr(k), ld["k"], _ptr(v),
+            ld["v"], _ptr(q_norm_w), _ptr(k_norm_w), _ptr(positions), _ptr(rows), n_rows,
+            _ptr(q_out) if q is not None else None, ld["q_out"], _ptr(k_out) if k is not None else None, ld["k_out"],
+            _ptr(v_out) if v is not None else None, ld["v_out"], _ptr(err))
+    return q_out, k_out, v_out
+
+
+def _tree_rows(N, T, D, H_kv, dev, **tensors):
+    """Token strides of the nodes' tensors [N*T][heads][D]."""
+    strides = []
+    for name, t in tensors.items():
+        if t is None:
+            strides.append(0)
+            continue
+        H, d, ld = _heads(name, t, dev)
+        if d != D or t.shape[0] != N * T or (name.endswith("_tree") and H != H_kv):
+            raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
+        strides.append(ld)
+    return strides
+
+
+def attention_tree(q_hat, k_tree, v_tree, k_cache, v_cache, cache_len, parent=None, T: int | None = None, *, g=None,
+                   scale=None, out=None, workspace=None, err=None):
+    """gdn_attention_tree: q_hat [N*T][H_q][D] over the caches [N][cap][H_kv][D] (cache_len device int32 [N] rows
+    of each) and the nodes' own k_tree, v_tree [N*T][H_kv][D]; parent device int32 [N][T] (None: a chain,
+    then T is needed unless N*T tells it), g the gate [N*T][H_q][D] or None.  scale defaults to D ** -0.5.
+    Returns out [N*T][H_q*D] bf16."""
+    N, cap, H_kv, D = k_cache.shape
+    dev = k_cache.device
+    T = T if T is not None else parent.shape[1] if parent is not None else q_hat.shape[0] // max(N, 1)
+    H_q = q_hat.shape[1]
+    _want("k_cache", k_cache, torch.bfloat16, None, dev)
+    _want("v_cache", v_cache, torch.bfloat16, k_cache.shape, dev)
+    _want("cache_len", cache_len, torch.int32, (N,), dev)
+    _want("parent", parent, torch.int32, (N, T), dev)
+    ld_q, ld_kt, ld_vt, ld_g = _tree_rows(N, T, D, H_kv, dev, q_hat=q_hat, k_tree=k_tree, v_tree=v_tree, g=g)
+    if g is not None and g.shape[1] != H_q:
+        raise ValueError("g must have the heads of q_hat")
+    if out is None:
+        out = torch.empty(N * T, H_q * D, dtype=torch.bfloat16, device=dev)
+    _want("out", out, torch.bfloat16, (N * T, H_q * D), dev)
+    if workspace is None:
+        workspace = torch.empty(attention_tree_workspace_size(H_q, H_kv, D, N, T), dtype=torch.uint8, device=dev)
+    _run_on(dev, "gdn_attention_tree", _ptr(q_hat), ld_q, _ptr(k_tree), ld_kt, _ptr(v_tree), ld_vt, _ptr(k_cache),
+            _ptr(v_cache), cap, _ptr(cache_len), _ptr(parent), _ptr(g), ld_g, H_q, H_kv, D,
+            D ** -0.5 if scale is None else scale, N, T, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(err))
+    return out
+
+
+def attention_tree_workspace_size(H_q: int, H_kv: int, head_dim: int, N: int, T: int) -> int:
+    return int(load().gdn_attention_tree_workspace_size(H_q, H_kv, head_dim, N, T))
+
+
+def attn_tree_commit(k_tree, v_tree, T: int, parent, accepted, k_cache, v_cache, cache_len, *, cache_len_out=None,
+                     err=None):
+    """gdn_attn_tree_commit: the accepted paths' rows of k_tree, v_tree [N*T][H_kv][D] appended to the caches;
+    cache_len_out (default cache_len itself) becomes the new lengths.  Returns it."""
+    N, cap, H_kv, D = k_cache.shape
+    dev = k_cache.device
+    cache_len_out = cache_len if cache_len_out is None else cache_len_out
+    _want("k_cache", k_cache, torch.bfloat16, None, dev)
+    _want("v_cache", v_cache, torch.bfloat16, k_cache.shape, dev)
+    _want("parent", parent, torch.int32, (N, T), dev)
+    for name, t in (("accepted", accepted), ("cache_len", cache_len), ("cache_len_out", cache_len_out)):
+        _want(name, t, torch.int32, (N,), dev)
+    ld_kt, ld_vt = _tree_rows(N, T, D, H_kv, dev, k_tree=k_tree, v_tree=v_tree)
+    _run_on(dev, "gdn_attn_tree_commit", _ptr(k_tree), ld_kt, _ptr(v_tree), ld_vt, H_kv, D, N, T, _ptr(parent),
+            _ptr(accepted), _ptr(k_cache), _ptr(v_cache), cap, _ptr(cache_len), _ptr(cache_len_out), _ptr(err))
+    return cache_len_out
+
+
+def layer_tree_workspace(L: GdnLayer, N: int, T: int, device):
+    """The workspace of layer_decode_tree, kept until layer_tree_commit."""
+    return torch.empty(int(load().gdn_layer_tree_workspace_size(L.H_k, L.H_v, N, T)), dtype=torch.uint8, device=device)
+
+
+def layer_decode_tree(L: GdnLayer, N: int, T: int, parent, x, state, conv_state, workspace, state_slot=None, *, y=None,
+                      err=None):
+    """gdn_layer_decode_tree: x [N*T][hidden] -> y; state and conv_state are read, `workspace` keeps the projection
+    for layer_tree_commit.  Returns y."""
+    slots, dev = _want_pool(L.H_k, L.H_v, state, conv_state)
+    _want("parent", parent, torch.int32, (N, T), dev)
+    _want("state_slot", state_slot, torch.int32, (N,), dev)
+    if y is None:
+        y = torch.empty(N * T, L.hidden, dtype=torch.bfloat16, device=dev)
+    _run_on(dev, "gdn_layer_decode_tree", ctypes.byref(L), N, T, _ptr(parent), _ptr(x), x.stride(0), _ptr(state),
+            _ptr(conv_state), _ptr(state_slot), slots, _ptr(y), y.stride(0), _ptr(workspace), workspace.numel(),
+            _ptr(err))
+    return y
+
+
+def layer_tree_commit(L: GdnLayer, N: int, T: int, parent, accepted, state, conv_state, workspace, state_slot=None, *,
+                      err=None):
+    """gdn_layer_tree_commit: state and conv_state advanced in place along the accepted paths of the
+    layer_decode_tree call that left `workspace`."""
+    slots, dev = _want_pool(L.H_k, L.H_v, state, conv_state)
+    _want("parent", parent, torch.int32, (N, T), dev)
+    _want("accepted", accepted, torch.int32, (N,), dev)
+    _want("state_slot", state_slot, torch.int32, (N,), dev)
+    _run_on(dev, "gdn_layer_tree_commit", ctypes.byref(L), N, T, _ptr(parent), _ptr(accepted), _ptr(state),
+            _ptr(conv_state), _ptr(state_slot), slots, _ptr(workspace), workspace.numel(), _ptr(err))
+
+
+def attn_layer_tree_workspace(N: int, T: int, device):
+    """The workspace of attn_layer_decode_tree, kept until attn_layer_tree_commit."""
+    return torch.empty(int(load().gdn_attn_layer_tree_workspace_size(N, T)), dtype=torch.uint8, device=device)
+
+
+def _want_attn_cache(N, k_cache, v_cache, cache_len):
+    shape = (N, k_cache.shape[1], ATTN_KV_HEADS, ATTN_HEAD_DIM)
+    _want("k_cache", k_cache, torch.bfloat16, shape)
+    _want("v_cache", v_cache, torch.bfloat16, shape, k_cache.device)
+    _want("cache_len", cache_len, torch.int32, (N,), k_cache.device)
+    return k_cache.device, shape[1]
+
+
+def attn_layer_decode_tree(L: GdnAttnLayer, N: int, T: int, parent, x, k_cache, v_cache, cache_len, workspace, *, y=None,
+                           err=None):
+    """gdn_attn_layer_decode_tree: x [N*T][hidden] -> y; the caches and cache_len are read, `workspace` keeps the
+    nodes' keys and values for attn_layer_tree_commit.  Returns y."""
+    dev, cap = _want_attn_cache(N, k_cache, v_cache, cache_len)
+    _want("parent", parent, torch.int32, (N, T), dev)
+    if y is None:
+        y = torch.empty(N * T, L.hidden, dtype=torch.bfloat16, device=dev)
+    _run_on(dev, "gdn_attn_layer_decode_tree", ctypes.byref(L), N, T, _ptr(parent), _ptr(x), x.stride(0), _ptr(k_cache),
+            _ptr(v_cache), cap, _ptr(cache_len), _ptr(y), y.stride(0), _ptr(workspace), workspace.numel(), _ptr(err))
+    return y
+
+
+def attn_layer_tree_commit(N: int, T: int, parent, accepted, k_cache, v_cache, cache_len, workspace, *, err=None):
+    """gdn_attn_layer_tree_commit: the accepted paths appended to the caches, cache_len advanced in place."""
+    dev, cap = _want_attn_cache(N, k_cache, v_cache, cache_len)
+    _want("parent", parent, torch.int32, (N, T), dev)
+    _want("accepted", accepted, torch.int32, (N,), dev)
+    _run_on(dev, "gdn_attn_layer_tree_commit", N, T, _ptr(parent), _ptr(accepted), _ptr(k_cache), _ptr(v_cache), cap,
+            _ptr(cache_len), _ptr(workspace), workspace.numel(), _ptr(err))
 
 
 def status_string(status: int) -> str:

@@ -40,7 +40,8 @@
  *     4 = cu_seqlens on the device disagreed with cu_seqlens_host, 8 = a decode
  *     state_slot outside the pool, 16 = an attention KV cache with no row left, 32 = an
  *     attention decode cache_len outside [0, cache_cap], 64 = (libgdn_debug.so only) a
- *     prefill kernel found a workspace access outside the workspace and skipped it).
+ *     prefill kernel found a workspace access outside the workspace and skipped it, 128 = a
+ *     tree's parent, an accepted node or a cache row of gdn_qk_norm_rope outside its range).
  *     It is never cleared by the library.  Read it after synchronising; gdn_err_status
  *     maps it to a gdn_status.
  *   - libgdn_debug.so exports the same calls, built with every workspace access of the
@@ -377,6 +378,178 @@ gdn_status gdn_attn_layer_decode_step(const gdn_attn_layer* L, int N, const void
 #define GDN_MAX_DECODE_TOKENS 8
 gdn_status gdn_decode_multi(const gdn_inputs* in, int N, int T, float* state, void* conv_state,
                             const int* state_slot, int n_slots, void* out, int* err, void* stream);
+
+/*
+ * Decoding with a TREE of drafted tokens: T = 1 .. GDN_MAX_TREE_NODES new tokens for each of N
+ * sequences, which need not follow one another.  Node t of sequence n is token n * T + t of the
+ * inputs, and
+ *   parent  device int32 [N][T] (NULL: a chain, parent t - 1 for node t)
+ * names the token it follows: -1 the last committed token, 0 .. t - 1 an earlier node of the
+ * same sequence.  Below -1 there is no node: the padding of a batch whose trees differ in size.
+ * A node whose parent is absent is absent too, and a parent >= t makes the node absent and sets
+ * bit 128 of *err.  An absent node's inputs are not used and its output row is zeros.
+ * Every node's result is that of decoding its path (its ancestors from the root on, then
+ * itself) after the committed tokens.  A verification call changes no state and no cache; the
+ * commit calls then take
+ *   accepted  device int32 [N], the last node of the accepted path, or -1 to accept none
+ * and advance the state or the cache along the path from the root to that node.  An accepted
+ * node that is absent or outside [-1, T) sets bit 128 of *err and counts as -1.
+ */
+#define GDN_MAX_TREE_NODES 64
+
+/*
+ * The delta-rule mixer for a tree: out bf16 [N * T][H_v][128], every node's output after its own
+ * path from the state and conv state as they stand (the causal conv runs along the path too).
+ * With G_t the sum of the path's log decays and e^{G_t - G_j} the decay from node j to t,
+ *   u_t = beta_t (v_t - e^{G_t} S k_t - sum over ancestors j of t: e^{G_t - G_j} (k_j . k_t) u_j)
+ *   o_t = e^{G_t} S q_t + sum over j = t and its ancestors: e^{G_t - G_j} (k_j . q_t) u_j,
+ * so the state is read once for all nodes.  The products run on the tensor cores with operands as
+ * bf16 pairs hi + lo (about 16 significant bits) and fp32 accumulation.
+ *   state       fp32 [n_slots][H_v][128][128], read
+ *   conv_state  bf16 [n_slots][3][C_conv], read
+ *   state_slot  as in gdn_decode_multi (NULL: sequence n uses slot n, n_slots >= N); slots may
+ *               repeat here.  A slot outside [0, n_slots) gives that sequence zero rows and sets bit 8.
+ * in->events, when set, gets 2 records as in decode.  N = 0 is a no-op.  out must not overlap the
+ * inputs, state, conv_state, state_slot or parent.
+ */
+gdn_status gdn_decode_tree(const gdn_inputs* in, int N, int T, const int* parent, const float* state,
+                           const void* conv_state, const int* state_slot, int n_slots, void* out, int* err,
+                           void* stream);
+
+/*
+ * The commit of gdn_decode_tree: applies the tokens of the accepted path, in order, exactly as
+ * gdn_decode_step calls would (same arithmetic: the states are bitwise those of decoding the
+ * path token by token).  in, N, T, parent: as in the gdn_decode_tree call (q and z are not read,
+ * but have to be valid).
+ *   state_in, conv_in    the pools as in gdn_decode_tree, read
+ *   state_out, conv_out  the pools written, the same slots; each either exactly its input (in place) or
+ *                        without overlap.  Slots no sequence uses stay as they were.
+ *   state_slot           slots must be distinct within a call
+ * A sequence that accepts nothing keeps its state (copied when not in place).
+ */
+gdn_status gdn_decode_tree_commit(const gdn_inputs* in, int N, int T, const int* parent, const int* accepted,
+                                  const float* state_in, float* state_out, const void* conv_in, void* conv_out,
+                                  const int* state_slot, int n_slots, int* err, void* stream);
+
+/*
+ * gdn_decode_tree between the layer's projections, as gdn_layer_decode: x bf16 [N*T][ldx] ->
+ * y bf16 [N*T][ldy].  The workspace keeps the projected inputs: pass it, unchanged, to
+ * gdn_layer_tree_commit, which advances state and conv_state in place along the accepted paths
+ * (one workspace per layer between the step and its commit).  y must not overlap the workspace, the
+ * state or the conv state.  L->events, when set, gets 4 records as in gdn_layer_prefill (the commit: none).
+ */
+size_t gdn_layer_tree_workspace_size(int H_k, int H_v, int N, int T);
+gdn_status gdn_layer_decode_tree(const gdn_layer* L, int N, int T, const int* parent, const void* x, long long ldx,
+                                 const float* state, const void* conv_state, const int* state_slot, int n_slots,
+                                 void* y, long long ldy, void* workspace, size_t workspace_bytes, int* err,
+                                 void* stream);
+gdn_status gdn_layer_tree_commit(const gdn_layer* L, int N, int T, const int* parent, const int* accepted,
+                                 float* state, void* conv_state, const int* state_slot, int n_slots,
+                                 const void* workspace, size_t workspace_bytes, int* err, void* stream);
+
+/*
+ * Rotary positions: pair i (of rotary_dim / 2) turns by position * theta_i,
+ *   layout   GDN_ROPE_HALF pairs dims (i, i + rotary_dim / 2), GDN_ROPE_INTERLEAVED (2 i, 2 i + 1);
+ *            dims from rotary_dim on are not turned
+ *   scaling  GDN_ROPE_NONE    theta_i = base^(-2 i / rotary_dim)
+ *            GDN_ROPE_LINEAR  theta_i / factor (positions interpolated)
+ *            GDN_ROPE_NTK     base * factor^(r / (r - 2)) in place of base, r = rotary_dim
+ *            GDN_ROPE_YARN    theta_i (1 - ramp_i) + theta_i / factor * ramp_i with ramp_i rising from 0 to 1
+ *                             between the pairs that turn beta_fast and beta_slow times within
+ *                             original_len positions, and cosine and sine times 0.1 ln(factor) + 1
+ * gdn_rope_init fills the table once; the struct is then only read.  turns[i] is theta_i / 2 pi in units of
+ * 2^-64 turns, so that position * turns[i] modulo 2^64 is the angle whatever the position: no angle of a
+ * far position loses bits before its reduction.  Positions may be any int32.
+ * head_dim: a multiple of 8, 8 .. GDN_ROPE_MAX_HEAD_DIM; rotary_dim: a multiple of 16, 0 .. head_dim (0: no
+ * rotation), else GDN_ERR_UNSUPPORTED; base > 1, factor >= 1 and finite, eps >= 0, and for YaRN original_len >= 1 and
+ * beta_fast > beta_slow > 0, else GDN_ERR_INVALID_ARG.
+ */
+#define GDN_ROPE_MAX_HEAD_DIM 256
+enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 };
+enum { GDN_ROPE_NONE = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_NTK = 2, GDN_ROPE_YARN = 3 };
+typedef struct {
+  int head_dim, rotary_dim;
+  int layout;
+  float eps;          /* of the norms */
+  float amplitude;    /* factor on cosine and sine */
+  unsigned long long turns[GDN_ROPE_MAX_HEAD_DIM / 2];
+} gdn_rope;
+gdn_status gdn_rope_init(gdn_rope* rope, int head_dim, int rotary_dim, int layout, int scaling, double base,
+                         double factor, int original_len, double beta_fast, double beta_slow, float eps);
+
+/*
+ * RMS norm of each head of q and k, the rotation of their positions, and the placement of k and v,
+ * in one pass over n_tok tokens:
+ *   q_out = rope(q / sqrt(mean q^2 + eps) * q_norm_w), k_out likewise with k_norm_w, v_out = v.
+ *   q, k, v        bf16 [n_tok][ld], heads of head_dim side by side (H_q, H_kv, H_kv of them); q may be
+ *                  NULL with H_q = 0, k NULL with v NULL and H_kv = 0, v NULL alone (v_out NULL too)
+ *   q_norm_w, k_norm_w   bf16 [head_dim], each NULL for no norm
+ *   positions      device int32 [n_tok], NULL: 0, 1, ..
+ *   rows           device int64 [n_tok], the row of k_out and v_out that token t goes to, NULL: row t (n_rows >= n_tok).
+ *                  Negative: not stored.  A row >= n_rows is not stored and sets bit 128 of *err.  Rows
+ *                  no token names stay as they were; two tokens that name one row race.
+ *   q_out bf16 [n_tok][ld_qo]; k_out [n_rows][ld_ko], v_out [n_rows][ld_vo]
+ * q_out may be exactly q with the same stride (in place), and without `rows` k_out exactly k; otherwise outputs
+ * overlap neither inputs nor one another.  The sums and rotations are fp32, one rounding to bf16 per output element.
+ */
+gdn_status gdn_qk_norm_rope(const gdn_rope* rope, long long n_tok, int H_q, int H_kv, const void* q, long long ld_q,
+                            const void* k, long long ld_k, const void* v, long long ld_v, const void* q_norm_w,
+                            const void* k_norm_w, const int* positions, const long long* rows, long long n_rows,
+                            void* q_out, long long ld_qo, void* k_out, long long ld_ko, void* v_out, long long ld_vo,
+                            int* err, void* stream);
+
+/*
+ * Attention of a tree's nodes over a KV cache: node t of sequence n sees rows 0 .. cache_len[n] - 1 of its
+ * cache and, among the nodes, its ancestors and itself:
+ *   out = softmax(scale q K^T) V * sigmoid(g), query head h reading KV head h / (H_q / H_kv).
+ *   q_hat           bf16 [N*T][ld_q], H_q heads of head_dim
+ *   k_tree, v_tree  bf16 [N*T][ld_kt], [N*T][ld_vt], H_kv heads: the nodes' own keys and values
+ *   k_cache, v_cache  bf16 [N][cache_cap][H_kv][head_dim]
+ *   cache_len       device int32 [N], rows in use, 0 <= cache_len[n] <= cache_cap (outside: zero
+ *                   rows for that sequence and bit 32 of *err)
+ *   g               bf16 [N*T][ld_g], H_q heads, or NULL for no gate
+ *   out             bf16 [N*T][H_q][head_dim]
+ * What rows beyond cache_len, absent nodes and nodes off a node's path hold (infinities and NaN
+ * included) does not reach its output.  head_dim is 128 or 256 and H_q / H_kv at most 16 (else
+ * GDN_ERR_UNSUPPORTED); scale > 0 and finite.  The probabilities enter the tensor cores as bf16 (relative error
+ * <= 2^-9 each), sums and statistics are fp32.  Repeated calls give bitwise equal results.
+ *   workspace  device scratch of gdn_attention_tree_workspace_size bytes, 16-byte aligned, not shared
+ *              with a call that may run at the same time; contents need no initialisation
+ */
+size_t gdn_attention_tree_workspace_size(int H_q, int H_kv, int head_dim, int N, int T);
+gdn_status gdn_attention_tree(const void* q_hat, long long ld_q, const void* k_tree, long long ld_kt,
+                              const void* v_tree, long long ld_vt, const void* k_cache, const void* v_cache,
+                              int cache_cap, const int* cache_len, const int* parent, const void* g, long long ld_g,
+                              int H_q, int H_kv, int head_dim, float scale, int N, int T, void* out, void* workspace,
+                              size_t workspace_bytes, int* err, void* stream);
+
+/*
+ * The commit of gdn_attention_tree: the keys and values of the accepted path's nodes go to rows cache_len[n],
+ * cache_len[n] + 1, .. of the caches, and cache_len_out[n] becomes cache_len[n] plus their number.
+ *   cache_len_out   device int32 [N]; may be exactly cache_len (in place)
+ * A path that does not fit the cache is not appended at all (the length stays) and sets bit 16 of *err; a
+ * cache_len outside [0, cache_cap] likewise, with bit 32.  Other arguments as in gdn_attention_tree.
+ */
+gdn_status gdn_attn_tree_commit(const void* k_tree, long long ld_kt, const void* v_tree, long long ld_vt, int H_kv,
+                                int head_dim, int N, int T, const int* parent, const int* accepted, void* k_cache,
+                                void* v_cache, int cache_cap, const int* cache_len, int* cache_len_out, int* err,
+                                void* stream);
+
+/*
+ * The attention layer for a tree: in_proj, q/k norm and rotary (node at depth d of its tree: position cache_len[n] + d,
+ * its root at cache_len[n]), attention over the cache and the tree, out_proj.  x bf16 [N*T][ldx] -> y bf16
+ * [N*T][ldy]; the caches [N][cache_cap][4][256] and cache_len are read.  The workspace keeps the nodes'
+ * keys and values: pass it, unchanged, to gdn_attn_layer_tree_commit, which appends the accepted paths to the caches and
+ * advances cache_len in place.  Errors as the calls above and gdn_attn_layer_decode_step.
+ */
+size_t gdn_attn_layer_tree_workspace_size(int N, int T);
+gdn_status gdn_attn_layer_decode_tree(const gdn_attn_layer* L, int N, int T, const int* parent, const void* x,
+                                      long long ldx, const void* k_cache, const void* v_cache, int cache_cap,
+                                      const int* cache_len, void* y, long long ldy, void* workspace,
+                                      size_t workspace_bytes, int* err, void* stream);
+gdn_status gdn_attn_layer_tree_commit(int N, int T, const int* parent, const int* accepted, void* k_cache,
+                                      void* v_cache, int cache_cap, int* cache_len, const void* workspace,
+                                      size_t workspace_bytes, int* err, void* stream);
 
 /*
  * Allocation-free prefill.  The pages have no counterpart to this call; it

@@ -1,0 +1,217 @@
+"""Host-side checks of the tree calls (no GPU needed): sizes, the rotary table, and refusals before any
+launch.  Addresses are made up; no call here reaches a launch."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from gated_delta_rule_81_b200 import build, gdn
+
+INVALID, UNSUPPORTED, MISALIGNED, ALIAS, WORKSPACE = 1, 2, 3, 4, 7
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return gdn.load()
+
+
+def fake_inputs(H_k=2, H_v=6):
+    s = gdn.GdnInputs()
+    for i, f in enumerate(("q", "k", "v", "a", "b", "z", "conv_w", "A_log", "norm_w")):
+        setattr(s, f, (i + 1) << 32)
+    s.stride_q = s.stride_k = H_k * 128
+    s.stride_v = s.stride_z = H_v * 128
+    s.stride_a = s.stride_b = H_v
+    s.H_k, s.H_v, s.scale = H_k, H_v, 1.0
+    return s
+
+
+STATE, CONV, OUT, PARENT, ACC, SLOT = (x << 36 for x in range(1, 7))
+
+
+def decode_tree(lib, inp=None, N=2, T=4, parent=PARENT, state=STATE, conv=CONV, slot=None, slots=2, out=OUT):
+    return lib.gdn_decode_tree(ctypes.byref(inp or fake_inputs()), N, T, parent, state, conv, slot, slots, out, None, None)
+
+
+def test_decode_tree_refusals(lib):
+    assert decode_tree(lib, N=0) == 0
+    assert decode_tree(lib, N=-1) == INVALID
+    assert decode_tree(lib, T=0) == INVALID
+    assert decode_tree(lib, T=65) == INVALID
+    assert decode_tree(lib, N=65536, slots=65536) == UNSUPPORTED
+    assert decode_tree(lib, slots=1) == INVALID          # slot n for sequence n needs N slots
+    assert decode_tree(lib, state=None) == INVALID
+    assert decode_tree(lib, out=None) == INVALID
+    assert decode_tree(lib, state=STATE + 4) == MISALIGNED
+    assert decode_tree(lib, parent=PARENT + 2) == MISALIGNED
+    assert decode_tree(lib, out=STATE + 64) == ALIAS
+    assert decode_tree(lib, out=CONV) == ALIAS
+    assert decode_tree(lib, out=PARENT) == ALIAS
+    inp = fake_inputs()
+    assert decode_tree(lib, inp, out=inp.v) == ALIAS
+    assert decode_tree(lib, inp, out=inp.conv_w) == ALIAS
+    inp.stride_q = 100
+    assert decode_tree(lib, inp) == INVALID
+    assert decode_tree(lib, fake_inputs(1, 9)) == UNSUPPORTED
+
+
+def commit(lib, inp=None, N=2, T=4, parent=PARENT, acc=ACC, s_in=STATE, s_out=STATE, c_in=CONV, c_out=CONV, slots=2):
+    return lib.gdn_decode_tree_commit(ctypes.byref(inp or fake_inputs()), N, T, parent, acc, s_in, s_out, c_in, c_out,
+                                      None, slots, None, None)
+
+
+def test_decode_tree_commit_refusals(lib):
+    assert commit(lib, N=0) == 0
+    assert commit(lib, acc=None) == INVALID
+    assert commit(lib, s_out=None) == INVALID
+    assert commit(lib, T=65) == INVALID
+    assert commit(lib, s_out=STATE + 65536) == ALIAS     # neither in place nor apart
+    assert commit(lib, c_out=CONV + 16) == ALIAS
+    assert commit(lib, c_out=STATE) == ALIAS
+    assert commit(lib, s_out=ACC) == ALIAS
+    assert commit(lib, s_out=fake_inputs().q) == ALIAS
+    assert commit(lib, c_in=CONV + 8, c_out=CONV + 8) == MISALIGNED
+
+
+def attention(lib, H=24, Hkv=4, D=256, scale=0.0625, N=2, T=4, cap=100, ld_q=None, ld_kt=None, out=OUT, ws=7 << 36, nb=None,
+              k=8 << 36, v=9 << 36, g=None, ld_g=0, q=10 << 36, ln=11 << 36):
+    nb = lib.gdn_attention_tree_workspace_size(H, Hkv, D, N, T) if nb is None else nb
+    return lib.gdn_attention_tree(q, H * D if ld_q is None else ld_q, 12 << 36, Hkv * D if ld_kt is None else ld_kt, 13 << 36, Hkv * D,
+                                  k, v, cap, ln, PARENT, g, ld_g, H, Hkv, D, scale, N, T, out, ws, nb, None, None)
+
+
+def test_attention_tree_refusals(lib):
+    assert attention(lib, N=0) == 0
+    assert attention(lib, D=64) == UNSUPPORTED
+    assert attention(lib, H=68, Hkv=4) == UNSUPPORTED
+    assert attention(lib, H=25) == INVALID
+    assert attention(lib, T=65) == INVALID
+    assert attention(lib, cap=0) == INVALID
+    for scale in (0.0, -1.0, math.inf, math.nan):
+        assert attention(lib, scale=scale) == INVALID
+    assert attention(lib, ld_q=24 * 256 - 8) == INVALID
+    assert attention(lib, ld_q=24 * 256 + 4) == MISALIGNED
+    assert attention(lib, k=(8 << 36) + 8) == MISALIGNED
+    assert attention(lib, g=14 << 36, ld_g=100) == INVALID
+    assert attention(lib, ln=None) == INVALID
+    assert attention(lib, nb=0) == WORKSPACE
+    assert attention(lib, ws=None) == WORKSPACE
+    assert attention(lib, out=8 << 36) == ALIAS
+    assert attention(lib, out=10 << 36) == ALIAS
+    assert attention(lib, ws=8 << 36) == ALIAS
+    assert attention(lib, out=7 << 36) == ALIAS
+    assert lib.gdn_attention_tree_workspace_size(24, 4, 64, 1, 1) == 0
+    assert lib.gdn_attention_tree_workspace_size(24, 5, 256, 1, 1) == 0
+    assert lib.gdn_attention_tree_workspace_size(24, 4, 256, 1, 65) == 0
+
+
+def append(lib, k=8 << 36, v=9 << 36, ln=11 << 36, lo=11 << 36, kt=12 << 36, D=256, cap=50, N=2, acc=ACC, ld=4 * 256):
+    return lib.gdn_attn_tree_commit(kt, ld, 13 << 36, 4 * 256, 4, D, N, 4, PARENT, acc, k, v, cap, ln, lo, None, None)
+
+
+def test_attn_tree_commit_refusals(lib):
+    assert append(lib, N=0) == 0
+    assert append(lib, acc=None) == INVALID
+    assert append(lib, cap=0) == INVALID
+    assert append(lib, ld=8) == INVALID
+    assert append(lib, D=96) == UNSUPPORTED
+    assert append(lib, v=8 << 36) == ALIAS
+    assert append(lib, kt=8 << 36) == ALIAS
+    assert append(lib, lo=(11 << 36) + 4) == ALIAS
+    assert append(lib, lo=8 << 36) == ALIAS
+    assert append(lib, k=(8 << 36) + 2) == MISALIGNED
+
+
+def rope_call(lib, rope=None, n=4, H=2, Hkv=1, q=1 << 36, ld_q=256, k=2 << 36, ld_k=128, v=3 << 36, ld_v=128, rows=None, n_rows=4,
+              qo=4 << 36, ld_qo=256, ko=5 << 36, ld_ko=128, vo=6 << 36, ld_vo=128):
+    rope = rope or gdn.make_rope(128, 64)
+    return lib.gdn_qk_norm_rope(ctypes.byref(rope), n, H, Hkv, q, ld_q, k, ld_k, v, ld_v, None, None, None, rows, n_rows, qo, ld_qo,
+                                ko, ld_ko, vo, ld_vo, None, None)
+
+
+def test_qk_norm_rope_refusals(lib):
+    assert rope_call(lib, n=0) == 0
+    assert rope_call(lib, H=0, Hkv=0, q=None, k=None, v=None, vo=None) == 0
+    assert rope_call(lib, gdn.GdnRope()) == INVALID      # never initialised
+    assert rope_call(lib, n=-1) == INVALID
+    assert rope_call(lib, q=None) == INVALID
+    assert rope_call(lib, v=None) == INVALID             # v_out without v
+    assert rope_call(lib, n_rows=3) == INVALID           # row t for token t needs n_tok rows
+    assert rope_call(lib, ld_q=128) == INVALID
+    assert rope_call(lib, ld_k=132) == MISALIGNED
+    assert rope_call(lib, qo=(4 << 36) + 2) == MISALIGNED
+    assert rope_call(lib, n=2 ** 31, n_rows=2 ** 31) == UNSUPPORTED
+    assert rope_call(lib, qo=(1 << 36) + 16) == ALIAS    # overlapping, not in place
+    assert rope_call(lib, ko=2 << 36, rows=7 << 36) == ALIAS  # in place under a permutation
+    assert rope_call(lib, vo=3 << 36) == ALIAS
+    assert rope_call(lib, vo=5 << 36) == ALIAS
+
+
+def test_rope_init(lib):
+    def init(D=128, R=128, layout=0, scaling=0, base=1e4, factor=1.0, orig=0, fast=32.0, slow=1.0, eps=1e-6):
+        rope = gdn.GdnRope()
+        return lib.gdn_rope_init(ctypes.byref(rope), D, R, layout, scaling, base, factor, orig, fast, slow, eps), rope
+    assert init()[0] == 0
+    assert init(D=130)[0] == UNSUPPORTED
+    assert init(D=512, R=64)[0] == UNSUPPORTED
+    assert init(R=72)[0] == UNSUPPORTED
+    assert init(R=144)[0] == INVALID
+    assert init(layout=2)[0] == INVALID
+    assert init(scaling=4)[0] == INVALID
+    assert init(base=1.0)[0] == INVALID
+    assert init(factor=0.5)[0] == INVALID
+    assert init(factor=math.inf)[0] == INVALID
+    assert init(eps=-1.0)[0] == INVALID
+    assert init(scaling=3, factor=4.0)[0] == INVALID     # no original length
+    assert init(scaling=3, factor=4.0, orig=4096, fast=1.0)[0] == INVALID
+    with pytest.raises(ValueError):
+        gdn.make_rope(128, scaling="cubic")
+
+
+@pytest.mark.parametrize("scaling", ["none", "linear", "ntk", "yarn"])
+@pytest.mark.parametrize("R", [16, 64, 256])
+def test_rope_table(lib, scaling, R):
+    """turns[i] / 2^64 is theta_i / 2 pi, to the rounding of the oracle's 64-bit frequency."""
+    kw = dict(scaling=scaling, factor=4.0, original_len=4096)
+    rope = gdn.make_rope(256, R, base=1e6, **kw)
+    theta, amp = oracle.tree.rope_frequencies(R, 1e6, **kw)
+    got = np.array([rope.turns[i] for i in range(R // 2)], dtype=np.float64) / 2.0 ** 64 * (2 * math.pi)
+    np.testing.assert_allclose(got, theta, rtol=1e-14, atol=2.0 ** -62)
+    assert rope.amplitude == np.float32(amp)
+    assert all(rope.turns[i] == 0 for i in range(R // 2, 128))
+
+
+def test_layer_tree_sizes_and_refusals(lib):
+    assert lib.gdn_layer_tree_workspace_size(16, 48, 2, 65) == 0
+    assert lib.gdn_layer_tree_workspace_size(16, 48, 1, 64) >= 64 * (16480 + 6144) * 2
+    assert lib.gdn_attn_layer_tree_workspace_size(1, 0) == 0
+    need = lib.gdn_layer_tree_workspace_size(2, 6, 2, 4)
+    L = gdn.GdnLayer()
+    for i, f in enumerate(("w_in", "w_out", "conv_w", "A_log", "norm_w")):
+        setattr(L, f, (i + 20) << 36)
+    L.ld_w_in, L.ld_w_out, L.H_k, L.H_v, L.hidden, L.scale = 128, 768, 2, 6, 128, 1.0
+
+    def call(x=30 << 36, y=31 << 36, ws=32 << 36, nb=need, T=4, ldy=128, state=STATE):
+        return lib.gdn_layer_decode_tree(ctypes.byref(L), 2, T, PARENT, x, 128, state, CONV, None, 2, y, ldy, ws, nb, None, None)
+    assert call(T=65) == INVALID
+    assert call(x=None) == INVALID
+    assert call(nb=need - 1) == WORKSPACE
+    assert call(ldy=64) == INVALID
+    assert call(y=32 << 36) == ALIAS
+    assert call(y=STATE) == ALIAS
+    assert call(state=32 << 36) == ALIAS
+    assert call(x=(30 << 36) + 2) == MISALIGNED
+    L.hidden = 100
+    assert call() == UNSUPPORTED
+    L.hidden = 128
+    assert lib.gdn_layer_tree_commit(ctypes.byref(L), 2, 4, PARENT, ACC, 32 << 36, CONV, None, 2, 32 << 36, need, None, None) == ALIAS
+    assert lib.gdn_layer_tree_commit(ctypes.byref(L), 2, 4, PARENT, ACC, STATE, CONV, None, 2, 32 << 36, 5, None, None) == WORKSPACE
+    assert lib.gdn_attn_layer_tree_commit(2, 4, PARENT, ACC, STATE, CONV, 9, SLOT, 32 << 36, 5, None, None) == WORKSPACE
+
+
+def test_tree_oracle_paths():
+    assert oracle.tree.paths([-1, 0, -1, 1, -2, 4, 2]) == [[0], [0, 1], [2], [0, 1, 3], [], [], [2, 6]]
+    assert oracle.tree.paths([0, -1]) == [[], [1]]
