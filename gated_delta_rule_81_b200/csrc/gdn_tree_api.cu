@@ -380,6 +380,8 @@ gdn_status gdn_attention_tree(const void* q_hat, long long ld_q, const void* k_t
   if (H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || cache_cap < 1 || !(scale > 0.f) || !isfinite(scale))
     return GDN_ERR_INVALID_ARG;
   if ((head_dim != 128 && head_dim != 256) || H_q / H_kv > 16 || H_kv > 4096) return GDN_ERR_UNSUPPORTED;
+  // a sequence's cache is one dimension of a TMA tensor map: its stride stays below 2^40 bytes
+  if (2LL * H_kv * head_dim * cache_cap >= (1LL << 40) || (ld_kt | ld_vt) >= (1LL << 32)) return GDN_ERR_UNSUPPORTED;
   if (N == 0) return GDN_OK;
   const long long T_tot = static_cast<long long>(N) * T;
   const long long wq = static_cast<long long>(H_q) * head_dim, wk = static_cast<long long>(H_kv) * head_dim;
