@@ -1,141 +1,507 @@
-// gdn_decode_tree: the delta-rule mixer's outputs of every node of a tree of drafted tokens.
+// gdn_decode_tree: the delta-rule mixer's outputs of every node of a tree of drafted tokens, from
+// one read of the state.
+//
+// Per value head, with G_t the sum of the log decays on node t's path, gamma_t = e^{G_t}, D_tj = e^{G_t - G_j} for
+// an ancestor j of t (or t itself), 0 otherwise:
+//   A_tj = beta_t D_tj (k_j . k_t) for j < t,   P_tj = D_tj (k_j . q_t)
+//   R_t = beta_t (v_t - gamma_t S k_t),   (I + A) U = R,   o_t = gamma_t S q_t + sum_j P_tj u_j
+// A is strictly lower triangular whatever the tree, because a parent comes before its children.  In
+// the kernel's orientation (rows = d_v of the state): X = S [K | Q]^T, U^T = R^T T^T with T = (I + A)^-1,
+// O^T = X_q diag(gamma) + U^T P^T, so everything after X is local to 16 state rows and stays in one warp's registers.
+//
+// A CTA takes one key head of one sequence and its value heads in turn (one value head per CTA while
+// there are few sequences).  Warps 0-7, 16 state rows each: the conv, norm and products of q and k at the start,
+// then per value head the conv of v, X, U, O and the gated norm.  One to four more warps (kSolvers) form T and P of the
+// next value head meanwhile.  The state goes from global memory straight into MMA operand registers, always four
+// of a head's eight 16-column steps ahead, across heads.
+//
+// The products are m16n8k16 bf16 MMAs: the state's 128 rows meet 2 T <= 128 columns once, which is too
+// little per CTA for a tcgen05 tile to pay for moving the fp32 state through shared memory as bf16 pairs.
+// Every operand is a pair hi + lo (hi hi + hi lo + lo hi, about 16 significant bits): the gated norm
+// amplifies the rounding of a sum whose terms nearly cancel, and plain bf16 operands leave the
+// mixer's bound.  Sums, gates and the solve are fp32, the sums of log decays fp64 (their differences over a
+// long path would lose bits).
+//
+// A node whose inputs are not finite: zeros stand in for its row of R and U, so that no zero weight meets an
+// infinity, and its own outputs and its descendants' become NaN; other nodes do not see it.
 #include "gdn_tree.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kTreeThreads = 128;  // thread = state row (d_v)
+constexpr int kWorkers = 256;            // threads of warps 0-7
+constexpr int kQkRow = 576;              // bytes of one node's k (or q): 8 steps x 4 lanes x (4 hi | 4 lo), and 64 more so
+                                         // that a quarter-warp's 16-byte reads of two rows fall into different banks
+constexpr int kVRow = 132;               // floats of a node's v (then o): lanes (g, c) read bank 8 c + g
+constexpr int kMaxHeads = 8;             // value heads per key head
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+template <int NT>
+struct TreeCfg {
+  static constexpr int TP = 8 * NT;                       // nodes, padded
+  static constexpr int KT = (TP + 15) / 16;               // 16-node steps
+  static constexpr int kSolvers = NT <= 2 ? 1 : NT == 4 ? 2 : 4;
+  static constexpr int kThreads = kWorkers + 32 * kSolvers;
+  static constexpr int kMinCtas = NT <= 4 ? 2 : 1;
+  static constexpr int MR = TP + 4;                       // floats of a row of the T x T matrices
+  static constexpr int IR = KT * 64 + (KT % 2 ? 0 : 64);  // bytes of a row of the T and P operand images
+  static constexpr int kOffKk = 2 * TP * kQkRow;          // k . k, then k . q
+  static constexpr int kOffA = kOffKk + 2 * TP * MR * 4;
+  static constexpr int kOffX = kOffA + TP * MR * 4;
+  static constexpr int kOffT = kOffX + TP * MR * 4;
+  static constexpr int kOffP = kOffT + TP * IR;
+  static constexpr int kOffV = kOffP + TP * IR;
+  static constexpr int kSmem = kOffV + TP * kVRow * 4;
+};
+
+__device__ __forceinline__ void bar_arrive(int id, int n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
-// One CTA per (value head, sequence).  Shared: q, k, u f32 [T][128] and K K^T, Q K^T f32 [T][T].
-__global__ void __launch_bounds__(kTreeThreads) decode_tree_kernel(TreeParams p) {
-  const int h = blockIdx.x, n = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = p.T, kh = h / (p.H_v / p.H_k);
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// hi and lo words of two values
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
+}
+
+// d += A B^T with A = ah + al and B's words b = (hi0, hi1, lo0, lo1)
+__device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint4& b) {
+  mma_16816(d, ah, b.x, b.y);
+  mma_16816(d, ah, b.z, b.w);
+  mma_16816(d, al, b.x, b.y);
+}
+
+// the causal conv and SiLU of 8 channels of a node: its own raw row and three before it on its path
+__device__ __forceinline__ void conv8(const uint4 (&x)[kTaps], const uint4 (&w)[4], float (&y)[8]) {
+  // w[i]: channels 2 i, 2 i + 1, four taps each
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint4& we = w[e >> 1];
+    const uint32_t w01 = e & 1 ? we.z : we.x, w23 = e & 1 ? we.w : we.y;
+    const float wt[kTaps] = {bf16_lo(w01), bf16_hi(w01), bf16_lo(w23), bf16_hi(w23)};
+    float s = 0.f;
+#pragma unroll
+    for (int tap = 0; tap < kTaps; ++tap) {
+      const uint32_t word = (&x[tap].x)[e >> 1];
+      s = fmaf(wt[tap], e & 1 ? bf16_hi(word) : bf16_lo(word), s);
+    }
+    y[e] = silu_f(s);
+  }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
+    decode_tree_kernel(const __grid_constant__ TreeParams p) {
+  using C = TreeCfg<NT>;
+  constexpr int TP = C::TP, KT = C::KT;
+  const int part = blockIdx.x, parts = gridDim.x, kh = blockIdx.y, n = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int T = p.T, HP = p.H_v / p.H_k / parts, hv0 = (kh * parts + part) * HP;
   const long long C_conv = static_cast<long long>(2 * p.H_k + p.H_v) * kD;
-  extern __shared__ __align__(16) float tree_sm[];
-  float* q_s = tree_sm;
-  float* k_s = q_s + T * kD;
-  float* u_s = k_s + T * kD;
-  float* kk_s = u_s + T * kD;
-  float* qk_s = kk_s + T * T;
-  __shared__ Tree tree;
-  __shared__ float alpha_s[kMaxNodes], beta_s[kMaxNodes], start_s[kMaxNodes];
   const int slot = p.state_slot ? p.state_slot[n] : n;
-  const bool bad = slot < 0 || slot >= p.n_slots;
-  if (warp == 0) tree_load(tree, p.parent, n, T, h == 0 ? p.err : nullptr);
-  if (bad) {
-    if (tid == 0 && h == 0 && p.err) atomicOr(p.err, kDevErrBadSlot);
-    for (int t = 0; t < T; ++t)
-      p.out[((static_cast<long long>(n) * T + t) * p.H_v + h) * kD + tid] = __float2bfloat16(0.f);
+  const bool leader = part == 0 && kh == 0;
+  if (slot < 0 || slot >= p.n_slots) {
+    if (tid == 0 && leader && p.err) atomicOr(p.err, kDevErrBadSlot);
+    for (int x = tid; x < T * HP * (kD / 8); x += C::kThreads) {
+      const int t = x / (HP * (kD / 8)), y = x % (HP * (kD / 8));
+      reinterpret_cast<uint4*>(p.out + ((static_cast<long long>(n) * T + t) * p.H_v + hv0) * kD)[y] = make_uint4(0u, 0u, 0u, 0u);
+    }
     return;
   }
-  __syncthreads();
-  // conv of each node along its path, one channel of q, k and v per thread
-  const bf16* hist = p.conv_in + static_cast<long long>(slot) * 3 * C_conv;
-#pragma unroll 1
-  for (int part = 0; part < 3; ++part) {
-    const bf16* x = part == 0 ? p.q : part == 1 ? p.k : p.v;
-    const long long ld = part == 0 ? p.sq : part == 1 ? p.sk : p.sv;
-    const long long c0 = static_cast<long long>(part == 2 ? h : kh) * kD + tid;
-    const long long ch = c0 + static_cast<long long>(part) * p.H_k * kD;
-    float* dst = part == 0 ? q_s : part == 1 ? k_s : u_s;
-    for (int t = 0; t < T; ++t) {
-      float y = 0.f;
-      int at = t;  // a node, or -1, -2, -3: history, latest first
-      if (tree.mask[t]) {
+  extern __shared__ __align__(16) uint8_t tsm[];
+  float* kk_s = reinterpret_cast<float*>(tsm + C::kOffKk);
+  float* a_s = reinterpret_cast<float*>(tsm + C::kOffA);
+  float* x_s = reinterpret_cast<float*>(tsm + C::kOffX);
+  float* v_s = reinterpret_cast<float*>(tsm + C::kOffV);
+  __shared__ Tree tree;
+  __shared__ int tap_s[kMaxNodes][kTaps - 1];        // node (or -1, -2, -3: history, latest first) 3, 2, 1 before
+  __shared__ float g_s[kMaxHeads][TP], beta_s[kMaxHeads][TP];
+  __shared__ float gamma_s[TP];
+  __shared__ double sum_s[TP];
+  __shared__ unsigned long long poison_s[kMaxHeads];  // nodes of each head whose R or U was not finite
+
+  // ---- this warp's state rows, 16-column step ks: lane (g, c) takes columns 16 ks + 4 c .. + 3 of rows g, g + 8
+  const float* S0 = p.state_in + (static_cast<long long>(slot) * p.H_v + hv0) * kD * kD;
+  float4 raw[4][2];
+  auto load_step = [&](int jh, int ks) {
+    const float* src = S0 + static_cast<long long>(jh) * kD * kD + (16 * warp + g) * kD + 16 * ks + 4 * c;
+    raw[ks & 3][0] = __ldcs(reinterpret_cast<const float4*>(src));
+    raw[ks & 3][1] = __ldcs(reinterpret_cast<const float4*>(src + 8 * kD));
+  };
+  if (warp < 8) {
 #pragma unroll
-        for (int tap = kTaps - 1; tap >= 0; --tap) {
-          const float xv = __bfloat162float(at >= 0 ? x[(static_cast<long long>(n) * T + at) * ld + c0]
-                                                    : hist[(3 + at) * C_conv + ch]);
-          y = fmaf(__bfloat162float(p.conv_w[ch * kTaps + tap]), xv, y);
-          at = at >= 0 ? tree.parent[at] : at - 1;
+    for (int ks = 0; ks < 4; ++ks) load_step(0, ks);
+  }
+
+  if (warp == 0) {
+    tree_load(tree, p.parent, n, T, leader ? p.err : nullptr);
+    for (int t = lane; t < T; t += 32) {
+      int at = t;
+#pragma unroll
+      for (int i = kTaps - 2; i >= 0; --i) {
+        at = at >= 0 ? max(tree.parent[at], -1) : at - 1;
+        tap_s[t][i] = max(at, -3);
+      }
+    }
+  }
+  if (tid < kMaxHeads) poison_s[tid] = 0ull;
+  for (int x = tid; x < TP * C::IR * 2 / 16; x += C::kThreads)  // T and P images (adjacent): what no node sees stays 0
+    reinterpret_cast<uint4*>(tsm + C::kOffT)[x] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
+
+  const bf16* hist = p.conv_in + static_cast<long long>(slot) * 3 * C_conv;
+  // raw rows of node t's conv window: 8 channels at `off` of tensor x, conv channel ch
+  auto window = [&](int t, const bf16* x, long long ld, long long off, long long ch, uint4 (&w)[kTaps]) {
+#pragma unroll
+    for (int i = 0; i < kTaps - 1; ++i) {
+      const int at = tap_s[t][i];
+      w[i] = *reinterpret_cast<const uint4*>(at >= 0 ? x + (static_cast<long long>(n) * T + at) * ld + off
+                                                     : hist + (3 + at) * C_conv + ch);
+    }
+    w[kTaps - 1] = *reinterpret_cast<const uint4*>(x + (static_cast<long long>(n) * T + t) * ld + off);
+  };
+
+  if (warp < 8) {
+    // ---- q (lanes 0-15) and k (16-31) of one node per warp: conv, SiLU, norm, split into the operand rows
+    const bool is_k = lane >= 16;
+    const int l = lane & 15;
+    const long long off = static_cast<long long>(kh) * kD + 8 * l, ch = off + (is_k ? static_cast<long long>(p.H_k) * kD : 0);
+    uint4 cw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cw[i] = reinterpret_cast<const uint4*>(p.conv_w + ch * kTaps)[i];
+    for (int t = warp; t < TP; t += 8) {
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (t < T && tree.mask[t]) {  // the same for the whole warp
+        uint4 w[kTaps];
+        window(t, is_k ? p.k : p.q, is_k ? p.sk : p.sq, off, ch, w);
+        conv8(w, cw, y);
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float f = rsqrtf(ss + 1e-6f) * (is_k ? 1.f : p.scale);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= f;
+      }
+      // dims 8 l .. + 7: step l / 2, lane slots c = 2 (l % 2) and + 1
+      uint8_t* dst = tsm + (is_k ? t : TP + t) * kQkRow + (l >> 1) * 64 + (l & 1) * 32;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4 v;
+        split2(y[4 * u], y[4 * u + 1], v.x, v.z);
+        split2(y[4 * u + 2], y[4 * u + 3], v.y, v.w);
+        reinterpret_cast<uint4*>(dst)[u] = v;
+      }
+    }
+  } else {
+    for (int x = tid - kWorkers; x < HP * TP; x += 32 * C::kSolvers) {
+      const int jh = x / TP, t = x % TP, h = hv0 + jh;
+      float gl = 0.f, be = 0.f;
+      if (t < T && tree.mask[t]) {
+        const long long tok = static_cast<long long>(n) * T + t;
+        gl = -expf(p.A_log[h]) * softplus_f(__bfloat162float(p.a[tok * p.sa + h]));
+        be = sigmoid_f(__bfloat162float(p.b[tok * p.sb + h]));
+      }
+      g_s[jh][t] = gl;
+      beta_s[jh][t] = be;
+    }
+  }
+  __syncthreads();
+  if (warp < 8) {
+    // ---- [K; Q] K^T: 16-row tile m of the 2 TP operand rows against 8 nodes j, where j can be an ancestor
+    for (int x = warp; x < NT * NT; x += 8) {
+      const int m = x / NT, jt = x % NT;
+      if (TP >= 16 && 8 * jt > (16 * m) % TP + 15) continue;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint8_t* ar = tsm + (16 * m + g) * kQkRow + c * 16;
+      const uint8_t* br = tsm + (8 * jt + g) * kQkRow + c * 16;
+#pragma unroll
+      for (int ks = 0; ks < kD / 16; ++ks) {
+        const uint4 r0 = *reinterpret_cast<const uint4*>(ar + ks * 64), r1 = *reinterpret_cast<const uint4*>(ar + 8 * kQkRow + ks * 64);
+        const uint4 b = *reinterpret_cast<const uint4*>(br + ks * 64);
+        const uint32_t ah[4] = {r0.x, r1.x, r0.y, r1.y}, al[4] = {r0.z, r1.z, r0.w, r1.w};
+        mma_split(d, ah, al, b);
+      }
+      float* dst = kk_s + (16 * m + g) * C::MR + 8 * jt + 2 * c;
+      *reinterpret_cast<float2*>(dst) = make_float2(d[0], d[1]);
+      *reinterpret_cast<float2*>(dst + 8 * C::MR) = make_float2(d[2], d[3]);
+    }
+  }
+  __syncthreads();
+
+  if (warp >= 8) {
+    // ------------------------------------------------ the solvers: T = (I + A)^-1 and P of each value head
+    constexpr int kSolve = 32 * C::kSolvers;
+    const int st = tid - kWorkers, sw = warp - 8;
+    for (int jh = 0; jh < HP; ++jh) {
+      if (jh > 0) named_bar_sync(2, C::kThreads);  // the workers have read the last head's T, P and gamma
+      if (sw == 0) {  // sums of log decays up each path, by pointer doubling
+        double acc[2];
+        int up[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = lane + 32 * e;
+          acc[e] = t < TP ? static_cast<double>(g_s[jh][t]) : 0.0;
+          up[e] = t < T && tree.mask[t] ? tree.parent[t] : -1;
+        }
+#pragma unroll 1
+        for (int i = 0; i < 6; ++i) {
+          double add[2];
+          int nu[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // the node `up` steps above, in whichever lane holds it
+            const int src = max(up[e], 0);
+            const double a0 = __shfl_sync(0xffffffffu, acc[0], src & 31), a1 = __shfl_sync(0xffffffffu, acc[1], src & 31);
+            const int u0 = __shfl_sync(0xffffffffu, up[0], src & 31), u1 = __shfl_sync(0xffffffffu, up[1], src & 31);
+            add[e] = up[e] >= 0 ? (src < 32 ? a0 : a1) : 0.0;
+            nu[e] = up[e] >= 0 ? (src < 32 ? u0 : u1) : -1;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            acc[e] += add[e];
+            up[e] = nu[e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = lane + 32 * e;
+          if (t < TP) {
+            sum_s[t] = acc[e];
+            gamma_s[t] = expf(static_cast<float>(acc[e]));
+          }
         }
       }
-      dst[t * kD + tid] = silu_f(y);
+      if (C::kSolvers > 1) named_bar_sync(4, kSolve); else __syncwarp();
+      for (int x = st; x < TP * TP; x += kSolve) {
+        const int t = x / TP, j = x % TP;
+        if (!((tree.mask[t] >> j) & 1)) continue;
+        const float dec = j == t ? 1.f : expf(static_cast<float>(sum_s[t] - sum_s[j]));
+        if (j < t) a_s[t * C::MR + j] = beta_s[jh][t] * dec * kk_s[t * C::MR + j];
+        const float pv = dec * kk_s[(TP + t) * C::MR + j];
+        const bf16 hi = __float2bfloat16(pv);
+        bf16* dst = reinterpret_cast<bf16*>(tsm + C::kOffP + t * C::IR + (j >> 4) * 64 + ((j & 7) >> 1) * 16 + ((j & 15) >> 3) * 4 + (j & 1) * 2);
+        dst[0] = hi;
+        dst[4] = __float2bfloat16(pv - __bfloat162float(hi));
+      }
+      if (C::kSolvers > 1) named_bar_sync(4, kSolve); else __syncwarp();
+      // row t of T is e_t - sum over its ancestors i of A_ti row i: 16 columns per warp, two lanes per column, each with
+      // every other ancestor
+      const int col = 16 * sw + (lane & 15), odd = lane >> 4;
+      const bool on = col < TP;
+      for (int t = 0; t < T; ++t) {
+        const unsigned long long mt = tree.mask[t];
+        unsigned long long anc = mt & ~(1ull << t);
+        float acc = 0.f;
+        if (odd) anc &= anc - 1;
+        while (anc) {
+          const int i = __ffsll(static_cast<long long>(anc)) - 1;
+          anc &= anc - 1;
+          anc &= anc - 1;
+          // row i holds column col where col is i or an ancestor of i, and is zero elsewhere
+          if (on && ((tree.mask[i] >> col) & 1)) acc = fmaf(-a_s[t * C::MR + i], x_s[i * C::MR + col], acc);
+        }
+        acc += __shfl_xor_sync(0xffffffffu, acc, 16);
+        if (col == t) acc = 1.f;
+        if (on && odd == 0 && ((mt >> col) & 1)) {
+          x_s[t * C::MR + col] = acc;
+          const bf16 hi = __float2bfloat16(acc);
+          bf16* dst = reinterpret_cast<bf16*>(tsm + C::kOffT + t * C::IR + (col >> 4) * 64 + ((col & 7) >> 1) * 16 + ((col & 15) >> 3) * 4 + (col & 1) * 2);
+          dst[0] = hi;
+          dst[4] = __float2bfloat16(acc - __bfloat162float(hi));
+        }
+        __syncwarp();
+      }
+      bar_arrive(3, C::kThreads);
     }
+    return;
   }
-  if (tid < T) {
-    const long long tok = static_cast<long long>(n) * T + tid;
-    alpha_s[tid] = tree.mask[tid] ? expf(-expf(p.A_log[h]) * softplus_f(__bfloat162float(p.a[tok * p.sa + h]))) : 0.f;
-    beta_s[tid] = tree.mask[tid] ? sigmoid_f(__bfloat162float(p.b[tok * p.sb + h])) : 0.f;
-  }
-  __syncthreads();
-  for (int x = warp; x < 2 * T; x += kTreeThreads / 32) {
-    float* row = (x & 1 ? k_s : q_s) + (x >> 1) * kD;
-    float ss = 0.f;
-    for (int j = lane; j < kD; j += 32) ss = fmaf(row[j], row[j], ss);
-    const float f = rsqrtf(warp_sum(ss) + 1e-6f) * (x & 1 ? 1.f : p.scale);
-    for (int j = lane; j < kD; j += 32) row[j] *= f;
-  }
-  __syncthreads();
-  for (int x = tid; x < T * T; x += kTreeThreads) {
-    const int t = x / T, j = x % T;
-    float kk = 0.f, qk = 0.f;
-    if ((tree.mask[t] >> j) & 1) {
-      for (int i = 0; i < kD; ++i) {
-        kk = fmaf(k_s[j * kD + i], k_s[t * kD + i], kk);
-        qk = fmaf(k_s[j * kD + i], q_s[t * kD + i], qk);
+
+  // ------------------------------------------------ the workers
+  float nw[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) nw[e] = __bfloat162float(p.norm_w[4 * lane + e]);  // norm_w: aligned to 2 bytes only
+  for (int jh = 0; jh < HP; ++jh) {
+    const int h = hv0 + jh;
+    // ---- v of this warp's 16 rows: a lane takes 8 channels of one node, 16 nodes at a time
+    {
+      const int piece = lane & 1;
+      const long long off = static_cast<long long>(h) * kD + 16 * warp + 8 * piece, ch = 2LL * p.H_k * kD + off;
+      uint4 cw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cw[i] = reinterpret_cast<const uint4*>(p.conv_w + ch * kTaps)[i];
+#pragma unroll 1
+      for (int t = lane >> 1; t < TP; t += 16) {
+        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (t < T && tree.mask[t]) {
+          uint4 w[kTaps];
+          window(t, p.v, p.sv, off, ch, w);
+          conv8(w, cw, y);
+        }
+        float4* dst = reinterpret_cast<float4*>(v_s + t * kVRow + 16 * warp + 8 * piece);
+        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
       }
     }
-    kk_s[x] = kk;
-    qk_s[x] = qk;
+    // ---- X = S [K | Q]^T; tile i < NT: nodes' keys, i >= NT: queries
+    float acc[2 * NT][4];
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < kD / 16; ++ks) {
+      uint32_t ah[4], al[4];
+      const float4 r0 = raw[ks & 3][0], r1 = raw[ks & 3][1];
+      split2(r0.x, r0.y, ah[0], al[0]);
+      split2(r1.x, r1.y, ah[1], al[1]);
+      split2(r0.z, r0.w, ah[2], al[2]);
+      split2(r1.z, r1.w, ah[3], al[3]);
+      if (ks < 4) load_step(jh, ks + 4);
+      else if (jh + 1 < HP) load_step(jh + 1, ks - 4);
+      const uint8_t* br = tsm + g * kQkRow + ks * 64 + c * 16;
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) mma_split(acc[i], ah, al, *reinterpret_cast<const uint4*>(br + 8 * i * kQkRow));
+    }
+    __syncwarp();                     // this warp's v_s columns
+    named_bar_sync(3, C::kThreads);   // T, P and gamma of this head
+    // ---- R^T = beta (v - gamma X_k), X_q *= gamma
+    float chk = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = 8 * i + 2 * c;
+      const float2 be = *reinterpret_cast<const float2*>(&beta_s[jh][t]), ga = *reinterpret_cast<const float2*>(&gamma_s[t]);
+      const float* v0 = v_s + t * kVRow + 16 * warp + g;
+      acc[i][0] = be.x * fmaf(-ga.x, acc[i][0], v0[0]);
+      acc[i][1] = be.y * fmaf(-ga.y, acc[i][1], v0[kVRow]);
+      acc[i][2] = be.x * fmaf(-ga.x, acc[i][2], v0[8]);
+      acc[i][3] = be.y * fmaf(-ga.y, acc[i][3], v0[kVRow + 8]);
+      acc[NT + i][0] *= ga.x;
+      acc[NT + i][1] *= ga.y;
+      acc[NT + i][2] *= ga.x;
+      acc[NT + i][3] *= ga.y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) chk = fmaf(acc[i][e], 0.f, chk);
+    }
+    auto clean = [&](float (&m)[NT][4]) {  // non-finite entries: their nodes are poisoned, zeros stand in
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!isfinite(m[i][e])) {
+            atomicOr(&poison_s[jh], 1ull << (8 * i + 2 * c + (e & 1)));
+            m[i][e] = 0.f;
+          }
+    };
+    float r[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[i][e] = acc[i][e];
+    if (chk != 0.f) clean(r);
+    // ---- U^T = R^T T^T: 16-node step kk reaches nodes from 16 kk on
+    float u[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[i][e] = 0.f;
+    auto times = [&](const float (&m)[NT][4], int off_img, float (&d)[NT][4]) {
+#pragma unroll
+      for (int kk = 0; kk < KT; ++kk) {
+        uint32_t ah[4], al[4];
+        split2(m[2 * kk][0], m[2 * kk][1], ah[0], al[0]);
+        split2(m[2 * kk][2], m[2 * kk][3], ah[1], al[1]);
+        if (2 * kk + 1 < NT) {
+          split2(m[(2 * kk + 1) % NT][0], m[(2 * kk + 1) % NT][1], ah[2], al[2]);
+          split2(m[(2 * kk + 1) % NT][2], m[(2 * kk + 1) % NT][3], ah[3], al[3]);
+        } else {
+          ah[2] = ah[3] = al[2] = al[3] = 0u;
+        }
+#pragma unroll
+        for (int i = 2 * kk; i < NT; ++i)
+          mma_split(d[i], ah, al, *reinterpret_cast<const uint4*>(tsm + off_img + (8 * i + g) * C::IR + kk * 64 + c * 16));
+      }
+    };
+    times(r, C::kOffT, u);
+    chk = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) chk = fmaf(u[i][e], 0.f, chk);
+    if (chk != 0.f) clean(u);
+    // ---- O^T = gamma X_q + U^T P^T, into shared memory (over this warp's own columns of v)
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = acc[NT + i][e];
+    times(u, C::kOffP, o);
+    if (jh + 1 < HP) bar_arrive(2, C::kThreads);  // T, P and gamma are free
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      float* dst = v_s + (8 * i + 2 * c) * kVRow + 16 * warp + g;
+      dst[0] = o[i][0];
+      dst[kVRow] = o[i][1];
+      dst[8] = o[i][2];
+      dst[kVRow + 8] = o[i][3];
+    }
+    named_bar_sync(1, kWorkers);
+    // ---- gated RMS norm, a warp per node
+    const unsigned long long poison = poison_s[jh];
+    for (int t = warp; t < T; t += 8) {
+      const long long tok = static_cast<long long>(n) * T + t;
+      const unsigned long long mask = tree.mask[t];
+      uint2 y = make_uint2(0u, 0u);
+      if (mask) {
+        const float4 ov = *reinterpret_cast<const float4*>(v_s + t * kVRow + 4 * lane);
+        const uint2 zz = *reinterpret_cast<const uint2*>(p.z + tok * p.sz + static_cast<long long>(h) * kD + 4 * lane);
+        float ss = fmaf(ov.x, ov.x, fmaf(ov.y, ov.y, fmaf(ov.z, ov.z, ov.w * ov.w)));
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+        const float inv = rsqrtf(ss * (1.0f / kD) + 1e-6f);
+        float f[4] = {ov.x * inv * nw[0] * silu_f(bf16_lo(zz.x)), ov.y * inv * nw[1] * silu_f(bf16_hi(zz.x)),
+                      ov.z * inv * nw[2] * silu_f(bf16_lo(zz.y)), ov.w * inv * nw[3] * silu_f(bf16_hi(zz.y))};
+        if (poison & mask) f[0] = f[1] = f[2] = f[3] = __int_as_float(0x7fffffff);
+        y = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+      }
+      *reinterpret_cast<uint2*>(p.out + (tok * p.H_v + h) * kD + 4 * lane) = y;
+    }
+    if (jh + 1 < HP) named_bar_sync(1, kWorkers);  // the next head's v overwrites o
   }
-  __syncthreads();
-  const float4* S = reinterpret_cast<const float4*>(p.state_in + ((static_cast<long long>(slot) * p.H_v + h) * kD + tid) * kD);
-  for (int t = 0; t < T; ++t) {
-    if (tree.mask[t] == 0) {
-      p.out[((static_cast<long long>(n) * T + t) * p.H_v + h) * kD + tid] = __float2bfloat16(0.f);
-      continue;
-    }
-    float sk = 0.f, sq = 0.f;
-    for (int i = 0; i < kD / 4; ++i) {
-      const float4 s = S[i];
-      const float4 kv = reinterpret_cast<const float4*>(k_s + t * kD)[i], qv = reinterpret_cast<const float4*>(q_s + t * kD)[i];
-      sk = fmaf(s.x, kv.x, fmaf(s.y, kv.y, fmaf(s.z, kv.z, fmaf(s.w, kv.w, sk))));
-      sq = fmaf(s.x, qv.x, fmaf(s.y, qv.y, fmaf(s.z, qv.z, fmaf(s.w, qv.w, sq))));
-    }
-    // up the path: w = e^{G_t - G_j}
-    float w = alpha_s[t], su = 0.f, so = 0.f;
-    for (int j = tree.parent[t]; j >= 0; j = tree.parent[j]) {
-      const float wu = w * u_s[j * kD + tid];
-      su = fmaf(kk_s[t * T + j], wu, su);
-      so = fmaf(qk_s[t * T + j], wu, so);
-      w *= alpha_s[j];
-    }
-    const float u = beta_s[t] * (u_s[t * kD + tid] - w * sk - su);
-    const float o = fmaf(w, sq, fmaf(qk_s[t * T + t], u, so));
-    u_s[t * kD + tid] = u;  // v_t made room for u_t: only this thread reads this column
-    // gated RMS norm over the 128 rows
-    start_s[warp] = 0.f;
-    __syncthreads();
-    const float ss = warp_sum(o * o);
-    if (lane == 0) start_s[warp] = ss;
-    __syncthreads();
-    const float inv = rsqrtf((start_s[0] + start_s[1] + start_s[2] + start_s[3]) * (1.0f / kD) + 1e-6f);
-    const long long tok = static_cast<long long>(n) * T + t;
-    const float z = __bfloat162float(p.z[tok * p.sz + static_cast<long long>(h) * kD + tid]);
-    p.out[(tok * p.H_v + h) * kD + tid] = __float2bfloat16(o * inv * __bfloat162float(p.norm_w[tid]) * silu_f(z));
-    __syncthreads();
-  }
+}
+
+template <int NT>
+cudaError_t launch_nt(const TreeParams& p, int parts, cudaStream_t stream) {
+  using C = TreeCfg<NT>;
+  const cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  decode_tree_kernel<NT><<<dim3(parts, p.H_k, p.N), C::kThreads, C::kSmem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream, void* const* events) {
-  const int smem = (3 * p.T * kD + 2 * p.T * p.T) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  int dev = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  // one CTA per value head while one per key head would leave SMs idle
+  const int parts = static_cast<long long>(p.N) * p.H_k < n_sm ? p.H_v / p.H_k : 1;
   if (events) cudaEventRecord(static_cast<cudaEvent_t>(events[0]), stream);
-  decode_tree_kernel<<<dim3(p.H_v, p.N), kTreeThreads, smem, stream>>>(p);
-  const cudaError_t e2 = cudaGetLastError();
+  e = p.T <= 8 ? launch_nt<1>(p, parts, stream)
+      : p.T <= 16 ? launch_nt<2>(p, parts, stream)
+      : p.T <= 32 ? launch_nt<4>(p, parts, stream)
+                  : launch_nt<8>(p, parts, stream);
   if (events) cudaEventRecord(static_cast<cudaEvent_t>(events[1]), stream);
-  return e2;
+  return e;
 }
 
 }  // namespace gdn
