@@ -11,9 +11,13 @@
 //
 // A CTA takes one key head of one sequence and its value heads in turn (one value head per CTA while
 // there are few sequences).  Warps 0-7, 16 state rows each: the conv, norm and products of q and k at the start,
-// then per value head the conv of v, X, U, O and the gated norm.  One to four more warps (kSolvers) form T and P of the
-// next value head meanwhile.  The state goes from global memory straight into MMA operand registers, always four
-// of a head's eight 16-column steps ahead, across heads.
+// then per value head the conv of v, X, U, O and the gated norm.  One to four more warps (kSolvers) form the next
+// value head's A, P and the inverses T_b of I + A's 16 x 16 diagonal blocks meanwhile; the workers solve block by block,
+//   U_b = T_b (R_b - sum over blocks b' < b of A_bb' U_b'),
+// with the same number of products as a multiplication by the whole inverse, which would have to be formed row by row (a
+// dependent chain of 60 rows took 30 to 200 thousand cycles per head).  The state goes from global
+// memory straight into MMA operand registers, always four of a head's eight 16-column steps ahead, across heads; raw
+// q, k and v rows come through shared memory by asynchronous copies, the next head's v during this head's products.
 //
 // The products are m16n8k16 bf16 MMAs: the state's 128 rows meet 2 T <= 128 columns once, which is too
 // little per CTA for a tcgen05 tile to pay for moving the fp32 state through shared memory as bf16 pairs.
@@ -39,19 +43,24 @@ constexpr int kMaxHeads = 8;             // value heads per key head
 template <int NT>
 struct TreeCfg {
   static constexpr int TP = 8 * NT;                       // nodes, padded
-  static constexpr int KT = (TP + 15) / 16;               // 16-node steps
+  static constexpr int KT = (TP + 15) / 16;               // 16-node blocks
   static constexpr int kSolvers = NT <= 2 ? 1 : NT == 4 ? 2 : 4;
   static constexpr int kThreads = kWorkers + 32 * kSolvers;
   static constexpr int kMinCtas = NT <= 4 ? 2 : 1;
-  static constexpr int MR = TP + 4;                       // floats of a row of the T x T matrices
-  static constexpr int IR = KT * 64 + (KT % 2 ? 0 : 64);  // bytes of a row of the T and P operand images
-  static constexpr int kOffKk = 2 * TP * kQkRow;          // k . k, then k . q
-  static constexpr int kOffA = kOffKk + 2 * TP * MR * 4;
-  static constexpr int kOffX = kOffA + TP * MR * 4;
-  static constexpr int kOffT = kOffX + TP * MR * 4;
-  static constexpr int kOffP = kOffT + TP * IR;
-  static constexpr int kOffV = kOffP + TP * IR;
-  static constexpr int kSmem = kOffV + TP * kVRow * 4;
+  static constexpr int MR = TP + 4;                       // floats of a row of the T x T products
+  static constexpr int IR = KT * 64 + (KT % 2 ? 0 : 64);  // bytes of a row of an operand image
+  // shared memory: [k; q] operand rows | k . k, then k . q | raw v rows | images and o, or at first raw q | k rows
+  static constexpr int kOffKk = 2 * TP * kQkRow;
+  static constexpr int kOffVraw = kOffKk + 2 * TP * MR * 4;
+  static constexpr int kVrawWarp = (TP + 3) * 32;         // 16 channels of each row, per warp
+  static constexpr int kOffM = kOffVraw + 8 * kVrawWarp;  // -A off the diagonal blocks, T_b in them
+  static constexpr int kOffP = kOffM + TP * IR;
+  static constexpr int kOffD = kOffP + TP * IR;           // A's diagonal blocks, f32 [KT][16][20]
+  static constexpr int kOffV = kOffD + KT * 16 * 20 * 4;
+  static constexpr int kEnd = kOffV + TP * kVRow * 4;
+  static constexpr int kOffRaw = kOffM;                   // [3 + TP][q 128 | k 128], until q and k are formed
+  static constexpr int kRawEnd = kOffRaw + (TP + 3) * 512;
+  static constexpr int kSmem = kEnd > kRawEnd ? kEnd : kRawEnd;
 };
 
 __device__ __forceinline__ void bar_arrive(int id, int n) {
@@ -92,7 +101,7 @@ __device__ __forceinline__ void conv8(const uint4 (&x)[kTaps], const uint4 (&w)[
       const uint32_t word = (&x[tap].x)[e >> 1];
       s = fmaf(wt[tap], e & 1 ? bf16_hi(word) : bf16_lo(word), s);
     }
-    y[e] = silu_f(s);
+    y[e] = silu_fast(s);
   }
 }
 
@@ -117,15 +126,14 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
   }
   extern __shared__ __align__(16) uint8_t tsm[];
   float* kk_s = reinterpret_cast<float*>(tsm + C::kOffKk);
-  float* a_s = reinterpret_cast<float*>(tsm + C::kOffA);
-  float* x_s = reinterpret_cast<float*>(tsm + C::kOffX);
+  float* d_s = reinterpret_cast<float*>(tsm + C::kOffD);
   float* v_s = reinterpret_cast<float*>(tsm + C::kOffV);
   __shared__ Tree tree;
-  __shared__ int tap_s[kMaxNodes][kTaps - 1];        // node (or -1, -2, -3: history, latest first) 3, 2, 1 before
+  __shared__ int tap_s[kMaxNodes][kTaps - 1];         // staged rows 3, 2, 1 before the node's own (t + 3) on its path
   __shared__ float g_s[kMaxHeads][TP], beta_s[kMaxHeads][TP];
   __shared__ float gamma_s[TP];
-  __shared__ double sum_s[TP];
-  __shared__ unsigned long long poison_s[kMaxHeads];  // nodes of each head whose R or U was not finite
+  __shared__ float2 sum_s[TP];                        // G as hi + lo
+  __shared__ unsigned long long poison_s[kMaxHeads];  // nodes of each head whose A, R or U was not finite
 
   // ---- this warp's state rows, 16-column step ks: lane (g, c) takes columns 16 ks + 4 c .. + 3 of rows g, g + 8
   const float* S0 = p.state_in + (static_cast<long long>(slot) * p.H_v + hv0) * kD * kD;
@@ -135,52 +143,62 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
     raw[ks & 3][0] = __ldcs(reinterpret_cast<const float4*>(src));
     raw[ks & 3][1] = __ldcs(reinterpret_cast<const float4*>(src + 8 * kD));
   };
+  const bf16* hist = p.conv_in + static_cast<long long>(slot) * 3 * C_conv;
+  const long long tok0 = static_cast<long long>(n) * T;
+  // staged row i: conv history oldest first, then the nodes' raw rows
+  for (int x = tid; x < (T + 3) * 32; x += C::kThreads) {
+    const int i = x >> 5, l = x & 15;
+    const bool is_k = x & 16;
+    const long long off = static_cast<long long>(kh) * kD + 8 * l;
+    const bf16* src = i < 3 ? hist + i * C_conv + (is_k ? static_cast<long long>(p.H_k) * kD : 0) + off
+                            : (is_k ? p.k + (tok0 + i - 3) * p.sk : p.q + (tok0 + i - 3) * p.sq) + off;
+    cp_async16(tsm + C::kOffRaw + x * 16, src);
+  }
+  uint8_t* vraw = tsm + C::kOffVraw + (warp & 7) * C::kVrawWarp;  // this worker's own
+  auto stage_v = [&](int jh) {
+    const long long off = static_cast<long long>(hv0 + jh) * kD + 16 * warp + 8 * (lane & 1);
+    for (int i = lane >> 1; i < T + 3; i += 16)
+      cp_async16(vraw + i * 32 + (lane & 1) * 16,
+                 i < 3 ? hist + i * C_conv + 2LL * p.H_k * kD + off : p.v + (tok0 + i - 3) * p.sv + off);
+  };
+  if (warp < 8) stage_v(0);
+  cp_async_commit();
   if (warp < 8) {
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) load_step(0, ks);
   }
-
-  if (warp == 0) {
+  if (warp == 8) {
     tree_load(tree, p.parent, n, T, leader ? p.err : nullptr);
     for (int t = lane; t < T; t += 32) {
       int at = t;
 #pragma unroll
       for (int i = kTaps - 2; i >= 0; --i) {
         at = at >= 0 ? max(tree.parent[at], -1) : at - 1;
-        tap_s[t][i] = max(at, -3);
+        tap_s[t][i] = max(at, -3) + 3;
       }
     }
   }
   if (tid < kMaxHeads) poison_s[tid] = 0ull;
-  for (int x = tid; x < TP * C::IR * 2 / 16; x += C::kThreads)  // T and P images (adjacent): what no node sees stays 0
-    reinterpret_cast<uint4*>(tsm + C::kOffT)[x] = make_uint4(0u, 0u, 0u, 0u);
+  cp_async_wait_all();
   __syncthreads();
-
-  const bf16* hist = p.conv_in + static_cast<long long>(slot) * 3 * C_conv;
-  // raw rows of node t's conv window: 8 channels at `off` of tensor x, conv channel ch
-  auto window = [&](int t, const bf16* x, long long ld, long long off, long long ch, uint4 (&w)[kTaps]) {
-#pragma unroll
-    for (int i = 0; i < kTaps - 1; ++i) {
-      const int at = tap_s[t][i];
-      w[i] = *reinterpret_cast<const uint4*>(at >= 0 ? x + (static_cast<long long>(n) * T + at) * ld + off
-                                                     : hist + (3 + at) * C_conv + ch);
-    }
-    w[kTaps - 1] = *reinterpret_cast<const uint4*>(x + (static_cast<long long>(n) * T + t) * ld + off);
-  };
 
   if (warp < 8) {
     // ---- q (lanes 0-15) and k (16-31) of one node per warp: conv, SiLU, norm, split into the operand rows
     const bool is_k = lane >= 16;
     const int l = lane & 15;
-    const long long off = static_cast<long long>(kh) * kD + 8 * l, ch = off + (is_k ? static_cast<long long>(p.H_k) * kD : 0);
+    const long long ch = static_cast<long long>(kh) * kD + 8 * l + (is_k ? static_cast<long long>(p.H_k) * kD : 0);
     uint4 cw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) cw[i] = reinterpret_cast<const uint4*>(p.conv_w + ch * kTaps)[i];
+    const uint8_t* rows = tsm + C::kOffRaw + lane * 16;
+#pragma unroll 2
     for (int t = warp; t < TP; t += 8) {
       float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (t < T && tree.mask[t]) {  // the same for the whole warp
         uint4 w[kTaps];
-        window(t, is_k ? p.k : p.q, is_k ? p.sk : p.sq, off, ch, w);
+#pragma unroll
+        for (int i = 0; i < kTaps; ++i)
+          w[i] = *reinterpret_cast<const uint4*>(rows + (i < kTaps - 1 ? tap_s[t][i] : t + 3) * 512);
         conv8(w, cw, y);
         float ss = 0.f;
 #pragma unroll
@@ -206,9 +224,8 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
       const int jh = x / TP, t = x % TP, h = hv0 + jh;
       float gl = 0.f, be = 0.f;
       if (t < T && tree.mask[t]) {
-        const long long tok = static_cast<long long>(n) * T + t;
-        gl = -expf(p.A_log[h]) * softplus_f(__bfloat162float(p.a[tok * p.sa + h]));
-        be = sigmoid_f(__bfloat162float(p.b[tok * p.sb + h]));
+        gl = -expf(p.A_log[h]) * softplus_f(__bfloat162float(p.a[(tok0 + t) * p.sa + h]));
+        be = sigmoid_f(__bfloat162float(p.b[(tok0 + t) * p.sb + h]));
       }
       g_s[jh][t] = gl;
       beta_s[jh][t] = be;
@@ -216,33 +233,55 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
   }
   __syncthreads();
   if (warp < 8) {
-    // ---- [K; Q] K^T: 16-row tile m of the 2 TP operand rows against 8 nodes j, where j can be an ancestor
-    for (int x = warp; x < NT * NT; x += 8) {
-      const int m = x / NT, jt = x % NT;
-      if (TP >= 16 && 8 * jt > (16 * m) % TP + 15) continue;
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint8_t* ar = tsm + (16 * m + g) * kQkRow + c * 16;
-      const uint8_t* br = tsm + (8 * jt + g) * kQkRow + c * 16;
+    // ---- [K; Q] K^T: 16-row tile m of the 2 TP operand rows against the nodes j that can be ancestors of its
+    // nodes, the tiles j shared by 8 / NT warps
+    const int m = warp % NT, jt0 = warp / NT;
+    constexpr int kStep = 8 / NT, kMine = (NT + kStep - 1) / kStep;
+    const int t_max = TP >= 16 ? (16 * m) % TP + 15 : TP - 1;
+    float d[kMine][4];
 #pragma unroll
+    for (int i = 0; i < kMine; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[i][e] = 0.f;
+    if (jt0 < NT) {
+      const uint8_t* ar = tsm + (16 * m + g) * kQkRow + c * 16;
+      const uint8_t* br = tsm + (8 * jt0 + g) * kQkRow + c * 16;
+#pragma unroll 2
       for (int ks = 0; ks < kD / 16; ++ks) {
         const uint4 r0 = *reinterpret_cast<const uint4*>(ar + ks * 64), r1 = *reinterpret_cast<const uint4*>(ar + 8 * kQkRow + ks * 64);
-        const uint4 b = *reinterpret_cast<const uint4*>(br + ks * 64);
         const uint32_t ah[4] = {r0.x, r1.x, r0.y, r1.y}, al[4] = {r0.z, r1.z, r0.w, r1.w};
-        mma_split(d, ah, al, b);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          if (jt0 + i * kStep < NT && 8 * (jt0 + i * kStep) <= t_max)
+            mma_split(d[i], ah, al, *reinterpret_cast<const uint4*>(br + 8 * i * kStep * kQkRow + ks * 64));
       }
-      float* dst = kk_s + (16 * m + g) * C::MR + 8 * jt + 2 * c;
-      *reinterpret_cast<float2*>(dst) = make_float2(d[0], d[1]);
-      *reinterpret_cast<float2*>(dst + 8 * C::MR) = make_float2(d[2], d[3]);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        if (jt0 + i * kStep < NT) {
+          float* dst = kk_s + (16 * m + g) * C::MR + 8 * (jt0 + i * kStep) + 2 * c;
+          *reinterpret_cast<float2*>(dst) = make_float2(d[i][0], d[i][1]);
+          *reinterpret_cast<float2*>(dst + 8 * C::MR) = make_float2(d[i][2], d[i][3]);
+        }
     }
+  } else {
+    // what no node sees stays zero in the images
+    for (int x = tid - kWorkers; x < (C::kOffV - C::kOffM) / 16; x += 32 * C::kSolvers)
+      reinterpret_cast<uint4*>(tsm + C::kOffM)[x] = make_uint4(0u, 0u, 0u, 0u);
   }
   __syncthreads();
 
   if (warp >= 8) {
-    // ------------------------------------------------ the solvers: T = (I + A)^-1 and P of each value head
+    // ------------------------------------------------ the solvers: A, P and the diagonal blocks' inverses of each value head
     constexpr int kSolve = 32 * C::kSolvers;
     const int st = tid - kWorkers, sw = warp - 8;
+    // byte offset of element (row t, column j) in an image: the four columns of a lane side by side, hi then lo
+    auto img = [](int t, int j) { return t * C::IR + (j >> 4) * 64 + ((j & 7) >> 1) * 16 + ((j & 15) >> 3) * 4 + (j & 1) * 2; };
+    auto put = [](uint8_t* at, float v) {
+      const bf16 hi = __float2bfloat16(v);
+      reinterpret_cast<bf16*>(at)[0] = hi;
+      reinterpret_cast<bf16*>(at)[4] = __float2bfloat16(v - __bfloat162float(hi));
+    };
     for (int jh = 0; jh < HP; ++jh) {
-      if (jh > 0) named_bar_sync(2, C::kThreads);  // the workers have read the last head's T, P and gamma
       if (sw == 0) {  // sums of log decays up each path, by pointer doubling
         double acc[2];
         int up[2];
@@ -253,7 +292,7 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
           up[e] = t < T && tree.mask[t] ? tree.parent[t] : -1;
         }
 #pragma unroll 1
-        for (int i = 0; i < 6; ++i) {
+        while (__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) {
           double add[2];
           int nu[2];
 #pragma unroll
@@ -270,54 +309,62 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
             up[e] = nu[e];
           }
         }
+        if (jh > 0) named_bar_sync(2, C::kThreads - (kSolve - 32));  // the workers have read the last head's images
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int t = lane + 32 * e;
           if (t < TP) {
-            sum_s[t] = acc[e];
-            gamma_s[t] = expf(static_cast<float>(acc[e]));
+            const float hi = static_cast<float>(acc[e]);
+            sum_s[t] = make_float2(hi, static_cast<float>(acc[e] - static_cast<double>(hi)));
+            gamma_s[t] = expf(hi);
           }
         }
       }
       if (C::kSolvers > 1) named_bar_sync(4, kSolve); else __syncwarp();
+#pragma unroll 4
       for (int x = st; x < TP * TP; x += kSolve) {
         const int t = x / TP, j = x % TP;
-        if (!((tree.mask[t] >> j) & 1)) continue;
-        const float dec = j == t ? 1.f : expf(static_cast<float>(sum_s[t] - sum_s[j]));
-        if (j < t) a_s[t * C::MR + j] = beta_s[jh][t] * dec * kk_s[t * C::MR + j];
-        const float pv = dec * kk_s[(TP + t) * C::MR + j];
-        const bf16 hi = __float2bfloat16(pv);
-        bf16* dst = reinterpret_cast<bf16*>(tsm + C::kOffP + t * C::IR + (j >> 4) * 64 + ((j & 7) >> 1) * 16 + ((j & 15) >> 3) * 4 + (j & 1) * 2);
-        dst[0] = hi;
-        dst[4] = __float2bfloat16(pv - __bfloat162float(hi));
+        const bool seen = (tree.mask[t] >> j) & 1;
+        const float2 gt = sum_s[t], gj = sum_s[j];
+        const float dec = j == t ? 1.f : __expf((gt.x - gj.x) + (gt.y - gj.y));
+        const float kk = kk_s[t * C::MR + j], qk = kk_s[(TP + t) * C::MR + j];
+        float av = beta_s[jh][t] * dec * kk;
+        if (seen) {
+          put(tsm + C::kOffP + img(t, j), dec * qk);
+          if (j < t) {
+            if (!isfinite(av)) {
+              atomicOr(&poison_s[jh], 1ull << t);
+              av = 0.f;
+            }
+            if ((t >> 4) == (j >> 4)) d_s[(t >> 4) * 320 + (t & 15) * 20 + (j & 15)] = av;
+            else put(tsm + C::kOffM + img(t, j), -av);
+          }
+        }
       }
       if (C::kSolvers > 1) named_bar_sync(4, kSolve); else __syncwarp();
-      // row t of T is e_t - sum over its ancestors i of A_ti row i: 16 columns per warp, two lanes per column, each with
-      // every other ancestor
-      const int col = 16 * sw + (lane & 15), odd = lane >> 4;
-      const bool on = col < TP;
-      for (int t = 0; t < T; ++t) {
-        const unsigned long long mt = tree.mask[t];
-        unsigned long long anc = mt & ~(1ull << t);
-        float acc = 0.f;
-        if (odd) anc &= anc - 1;
-        while (anc) {
-          const int i = __ffsll(static_cast<long long>(anc)) - 1;
-          anc &= anc - 1;
-          anc &= anc - 1;
-          // row i holds column col where col is i or an ancestor of i, and is zero elsewhere
-          if (on && ((tree.mask[i] >> col) & 1)) acc = fmaf(-a_s[t * C::MR + i], x_s[i * C::MR + col], acc);
+      // T_b: a lane per column of a 16 x 16 block, x_t = e_t - sum_{i < t} A_ti x_i down the column in registers
+      if (sw * 2 < KT) {
+        const int b = 2 * sw + (lane >> 4), col = lane & 15;
+        if (b < KT && 16 * b + col < TP) {
+          const float* ab = d_s + b * 320;
+          float x[16];
+#pragma unroll
+          for (int t = 0; t < 16; ++t) {
+            float s = col == t ? 1.f : 0.f;
+#pragma unroll
+            for (int i4 = 0; i4 < (t + 3) / 4; ++i4) {
+              const float4 av = *reinterpret_cast<const float4*>(ab + t * 20 + 4 * i4);
+              if (4 * i4 < t) s = fmaf(-av.x, x[4 * i4], s);
+              if (4 * i4 + 1 < t) s = fmaf(-av.y, x[4 * i4 + 1], s);
+              if (4 * i4 + 2 < t) s = fmaf(-av.z, x[4 * i4 + 2], s);
+              if (4 * i4 + 3 < t) s = fmaf(-av.w, x[4 * i4 + 3], s);
+            }
+            x[t] = s;
+          }
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            if (16 * b + t < TP) put(tsm + C::kOffM + img(16 * b + t, 16 * b + col), x[t]);
         }
-        acc += __shfl_xor_sync(0xffffffffu, acc, 16);
-        if (col == t) acc = 1.f;
-        if (on && odd == 0 && ((mt >> col) & 1)) {
-          x_s[t * C::MR + col] = acc;
-          const bf16 hi = __float2bfloat16(acc);
-          bf16* dst = reinterpret_cast<bf16*>(tsm + C::kOffT + t * C::IR + (col >> 4) * 64 + ((col & 7) >> 1) * 16 + ((col & 15) >> 3) * 4 + (col & 1) * 2);
-          dst[0] = hi;
-          dst[4] = __float2bfloat16(acc - __bfloat162float(hi));
-        }
-        __syncwarp();
       }
       bar_arrive(3, C::kThreads);
     }
@@ -333,21 +380,33 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
     // ---- v of this warp's 16 rows: a lane takes 8 channels of one node, 16 nodes at a time
     {
       const int piece = lane & 1;
-      const long long off = static_cast<long long>(h) * kD + 16 * warp + 8 * piece, ch = 2LL * p.H_k * kD + off;
+      const long long ch = 2LL * p.H_k * kD + static_cast<long long>(h) * kD + 16 * warp + 8 * piece;
       uint4 cw[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) cw[i] = reinterpret_cast<const uint4*>(p.conv_w + ch * kTaps)[i];
+      if (jh > 0) {
+        cp_async_wait_all();
+        __syncwarp();
+      }
+      const uint8_t* rows = vraw + piece * 16;
 #pragma unroll 1
       for (int t = lane >> 1; t < TP; t += 16) {
         float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (t < T && tree.mask[t]) {
           uint4 w[kTaps];
-          window(t, p.v, p.sv, off, ch, w);
+#pragma unroll
+          for (int i = 0; i < kTaps; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(rows + (i < kTaps - 1 ? tap_s[t][i] : t + 3) * 32);
           conv8(w, cw, y);
         }
         float4* dst = reinterpret_cast<float4*>(v_s + t * kVRow + 16 * warp + 8 * piece);
         dst[0] = make_float4(y[0], y[1], y[2], y[3]);
         dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+      }
+      __syncwarp();  // this warp's v_s columns; its raw rows are free
+      if (jh + 1 < HP) {
+        stage_v(jh + 1);
+        cp_async_commit();
       }
     }
     // ---- X = S [K | Q]^T; tile i < NT: nodes' keys, i >= NT: queries
@@ -370,9 +429,17 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
 #pragma unroll
       for (int i = 0; i < 2 * NT; ++i) mma_split(acc[i], ah, al, *reinterpret_cast<const uint4*>(br + 8 * i * kQkRow));
     }
-    __syncwarp();                     // this warp's v_s columns
-    named_bar_sync(3, C::kThreads);   // T, P and gamma of this head
-    // ---- R^T = beta (v - gamma X_k), X_q *= gamma
+    named_bar_sync(3, C::kThreads);  // images and gamma of this head
+    // non-finite entries: their nodes are poisoned, zeros stand in
+    auto clean = [&](float (&m)[4], int i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!isfinite(m[e])) {
+          atomicOr(&poison_s[jh], 1ull << (8 * i + 2 * c + (e & 1)));
+          m[e] = 0.f;
+        }
+    };
+    // ---- R^T = beta (v - gamma X_k), X_q *= gamma (the start of O^T)
     float chk = 0.f;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -390,88 +457,83 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
 #pragma unroll
       for (int e = 0; e < 4; ++e) chk = fmaf(acc[i][e], 0.f, chk);
     }
-    auto clean = [&](float (&m)[NT][4]) {  // non-finite entries: their nodes are poisoned, zeros stand in
+    if (chk != 0.f) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!isfinite(m[i][e])) {
-            atomicOr(&poison_s[jh], 1ull << (8 * i + 2 * c + (e & 1)));
-            m[i][e] = 0.f;
-          }
-    };
-    float r[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[i][e] = acc[i][e];
-    if (chk != 0.f) clean(r);
-    // ---- U^T = R^T T^T: 16-node step kk reaches nodes from 16 kk on
-    float u[NT][4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[i][e] = 0.f;
-    auto times = [&](const float (&m)[NT][4], int off_img, float (&d)[NT][4]) {
-#pragma unroll
-      for (int kk = 0; kk < KT; ++kk) {
-        uint32_t ah[4], al[4];
-        split2(m[2 * kk][0], m[2 * kk][1], ah[0], al[0]);
-        split2(m[2 * kk][2], m[2 * kk][3], ah[1], al[1]);
-        if (2 * kk + 1 < NT) {
-          split2(m[(2 * kk + 1) % NT][0], m[(2 * kk + 1) % NT][1], ah[2], al[2]);
-          split2(m[(2 * kk + 1) % NT][2], m[(2 * kk + 1) % NT][3], ah[3], al[3]);
-        } else {
-          ah[2] = ah[3] = al[2] = al[3] = 0u;
-        }
-#pragma unroll
-        for (int i = 2 * kk; i < NT; ++i)
-          mma_split(d[i], ah, al, *reinterpret_cast<const uint4*>(tsm + off_img + (8 * i + g) * C::IR + kk * 64 + c * 16));
+      for (int i = 0; i < NT; ++i) clean(acc[i], i);
+    }
+    // ---- block by block: U_b^T = R_b^T T_b^T, then its part of the later blocks' R and of O
+    auto split_tiles = [](const float (&m0)[4], const float (&m1)[4], bool two, uint32_t (&ah)[4], uint32_t (&al)[4]) {
+      split2(m0[0], m0[1], ah[0], al[0]);
+      split2(m0[2], m0[3], ah[1], al[1]);
+      if (two) {
+        split2(m1[0], m1[1], ah[2], al[2]);
+        split2(m1[2], m1[3], ah[3], al[3]);
+      } else {
+        ah[2] = ah[3] = al[2] = al[3] = 0u;
       }
     };
-    times(r, C::kOffT, u);
-    chk = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int b = 0; b < KT; ++b) {
+      constexpr bool kTwo = NT > 1;
+      const int i1 = kTwo ? 2 * b + 1 : 0;
+      const uint8_t* mb = tsm + C::kOffM + g * C::IR + b * 64 + c * 16;
+      const uint8_t* pb = tsm + C::kOffP + g * C::IR + b * 64 + c * 16;
+      uint32_t ah[4], al[4];
+      split_tiles(acc[2 * b], acc[i1], kTwo, ah, al);
+      float u[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      mma_split(u[0], ah, al, *reinterpret_cast<const uint4*>(mb + 16 * b * C::IR));
+      if (kTwo) mma_split(u[1], ah, al, *reinterpret_cast<const uint4*>(mb + (16 * b + 8) * C::IR));
+      chk = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) chk = fmaf(u[i][e], 0.f, chk);
-    if (chk != 0.f) clean(u);
-    // ---- O^T = gamma X_q + U^T P^T, into shared memory (over this warp's own columns of v)
-    float o[NT][4];
+      for (int e = 0; e < 4; ++e) chk = fmaf(u[0][e], 0.f, fmaf(u[1][e], 0.f, chk));
+      if (chk != 0.f) {
+        clean(u[0], 2 * b);
+        if (kTwo) clean(u[1], i1);
+      }
+      split_tiles(u[0], u[1], kTwo, ah, al);
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int i = 2 * b + 2; i < NT; ++i) mma_split(acc[i], ah, al, *reinterpret_cast<const uint4*>(mb + 8 * i * C::IR));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = acc[NT + i][e];
-    times(u, C::kOffP, o);
-    if (jh + 1 < HP) bar_arrive(2, C::kThreads);  // T, P and gamma are free
+      for (int i = 2 * b; i < NT; ++i) mma_split(acc[NT + i], ah, al, *reinterpret_cast<const uint4*>(pb + 8 * i * C::IR));
+    }
+    if (jh + 1 < HP) bar_arrive(2, kWorkers + 32);  // images and gamma are free
+    // ---- O^T into shared memory, over this warp's own columns of v
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       float* dst = v_s + (8 * i + 2 * c) * kVRow + 16 * warp + g;
-      dst[0] = o[i][0];
-      dst[kVRow] = o[i][1];
-      dst[8] = o[i][2];
-      dst[kVRow + 8] = o[i][3];
+      dst[0] = acc[NT + i][0];
+      dst[kVRow] = acc[NT + i][1];
+      dst[8] = acc[NT + i][2];
+      dst[kVRow + 8] = acc[NT + i][3];
+    }
+    uint2 zz[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = warp + 8 * i;
+      zz[i] = t < T ? *reinterpret_cast<const uint2*>(p.z + (tok0 + t) * p.sz + static_cast<long long>(h) * kD + 4 * lane)
+                    : make_uint2(0u, 0u);
     }
     named_bar_sync(1, kWorkers);
     // ---- gated RMS norm, a warp per node
     const unsigned long long poison = poison_s[jh];
-    for (int t = warp; t < T; t += 8) {
-      const long long tok = static_cast<long long>(n) * T + t;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = warp + 8 * i;
+      if (t >= T) break;
       const unsigned long long mask = tree.mask[t];
       uint2 y = make_uint2(0u, 0u);
       if (mask) {
         const float4 ov = *reinterpret_cast<const float4*>(v_s + t * kVRow + 4 * lane);
-        const uint2 zz = *reinterpret_cast<const uint2*>(p.z + tok * p.sz + static_cast<long long>(h) * kD + 4 * lane);
         float ss = fmaf(ov.x, ov.x, fmaf(ov.y, ov.y, fmaf(ov.z, ov.z, ov.w * ov.w)));
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
         const float inv = rsqrtf(ss * (1.0f / kD) + 1e-6f);
-        float f[4] = {ov.x * inv * nw[0] * silu_f(bf16_lo(zz.x)), ov.y * inv * nw[1] * silu_f(bf16_hi(zz.x)),
-                      ov.z * inv * nw[2] * silu_f(bf16_lo(zz.y)), ov.w * inv * nw[3] * silu_f(bf16_hi(zz.y))};
+        float f[4] = {ov.x * inv * nw[0] * silu_fast(bf16_lo(zz[i].x)), ov.y * inv * nw[1] * silu_fast(bf16_hi(zz[i].x)),
+                      ov.z * inv * nw[2] * silu_fast(bf16_lo(zz[i].y)), ov.w * inv * nw[3] * silu_fast(bf16_hi(zz[i].y))};
         if (poison & mask) f[0] = f[1] = f[2] = f[3] = __int_as_float(0x7fffffff);
         y = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
       }
-      *reinterpret_cast<uint2*>(p.out + (tok * p.H_v + h) * kD + 4 * lane) = y;
+      *reinterpret_cast<uint2*>(p.out + ((tok0 + t) * p.H_v + h) * kD + 4 * lane) = y;
     }
     if (jh + 1 < HP) named_bar_sync(1, kWorkers);  // the next head's v overwrites o
   }

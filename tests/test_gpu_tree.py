@@ -373,6 +373,26 @@ def test_decode_tree_large_batch_equals_its_sequences_alone():
     assert out_error(out[c["there"].cuda()], ref["out"][t]) <= OUT_TOL
 
 
+@pytest.mark.parametrize("key", ["q", "k", "v", "a", "b", "z"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T", [7, 16, 40])
+def test_decode_tree_infinities_stay_on_their_paths(key, value, T):
+    """A node whose input is not finite reaches its descendants (through its key, value or gates) or itself alone
+    (its query and output gate), and no other node."""
+    N, H_k, H_v, bad = 1, 2, 6, 2
+    c = delta_case(N, T, H_k, H_v, "holes", seed=31 + T)
+    clean = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"])
+    c["dev"][key][bad] = value
+    out = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"])
+    hit = torch.tensor([bad in p for p in oracle.tree.paths(c["rows"][0])], device="cuda")
+    assert bool(hit.any()) and bool((~hit).any())
+    assert torch.equal(out[~hit], clean[~hit])
+    if value != value and key != "z":
+        assert bool(torch.isnan(out[bad]).all())
+        if key in ("k", "v", "a", "b"):
+            assert bool(torch.isnan(out[hit]).all())
+
+
 def test_decode_tree_shared_and_bad_slots():
     N, T, H_k, H_v = 4, 6, 2, 6
     c = delta_case(N, T, H_k, H_v, "chain", seed=5, slots=6)
