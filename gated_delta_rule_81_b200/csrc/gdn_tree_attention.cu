@@ -5,19 +5,24 @@
 //   s_rj = scale q_r . k_j,  m_r = max_j s_rj,  o_r = sum_j e^{s_rj - m_r} v_j / sum_j e^{s_rj - m_r}
 // over the keys row r sees, the keys are taken once, in tiles of 64, with a running maximum and sum.
 //
-// Work split.  A unit is one (sequence, KV head): its tiles are ceil(cache_len / 64) tiles of the cache and
-// one tile of the tree.  The tiles of all units in a row are cut into W equal shares, one per
+// Work split.  A unit is one (sequence, KV head): its tiles are ceil(cache_len / 128) tiles of the cache and
+// one tile of the tree (64 keys).  The tiles of all units in a row are cut into W equal shares, one per
 // worker, so that ragged lengths balance and a single long sequence still fills the GPU; a unit cut between
 // workers leaves partial (o, m, l) that a second kernel joins.  Rows beyond 128 go to further CTAs (blockIdx.x)
 // of the same worker, which read the same tiles at about the same time, from L2.
 //
-// A CTA: warps 0-3 softmax and epilogue (thread = query row = TMEM lane), warp 4 TMA, warp 5 tcgen05.mma.
-// TMEM: O (D columns) | Q as bf16 pairs (D / 2) | S in two buffers of 64.  Q sits in tensor memory, so the
-// whole shared memory is a ring of K and V tiles: 6 stages of 32 KiB at D = 256, 12 of 16 KiB at D = 128.  Per tile j
-//   S_j = Q K_j^T (M 128, N 64, K = D, A from TMEM), P_j = exp2(S_j c - m) as bf16 over S_j's first
-//   32 columns, O += P_j V_j (M 128, N = D, K 64, A = P from TMEM, V MN-major),
+// A CTA: warps 0-7 softmax and epilogue (thread = query row = TMEM lane; warps w and w + 4 share a row's
+// 128 scores and O's D columns in halves), warp 8 TMA, warp 9 tcgen05.mma.  TMEM: O (D columns) | S in two buffers of
+// 128.  Shared memory: Q, and a ring of slots of 64 D elements (5 of 32 KiB at D = 256, 12 of 16 KiB at D = 128), which hold
+// half a K tile (128 keys x D / 2 dims) or half a V tile (64 keys x D) and are refilled as soon as their own products
+// have read them.  Per tile j
+//   S_j = Q K_j^T (M 128, N 128, K = D), P_j = exp2(S_j c - m) as bf16 over S_j's first 64 columns,
+//   O += P_j V_j (M 128, N = D, K 128, A = P from TMEM, V MN-major),
 // with S_{j+1} issued before P_j is awaited.  O and l are rescaled only when a row's maximum has grown by more than
-// 2^8; the final division by l makes the result the same.
+// 2^8; the final division by l makes the result the same.  Tiles of 64 keys with Q in TMEM (a ring of six 32 KiB tiles) took
+// 2450 cycles per 64 keys: an N = 64 product runs at 45 cycles per K step instead of 32, and the latency of the
+// S -> softmax -> P V round trip is paid twice as often.  The next unit's Q is fetched and its first S issued while
+// this one's epilogue runs.
 //
 // Whatever a row may not see contributes exactly nothing: masked scores become -inf by selection, so infinities
 // and NaN in masked keys vanish; masked values meet a zero probability in the product, so the
@@ -34,14 +39,14 @@ namespace gdn {
 
 namespace {
 
-constexpr int kBN = 64;              // keys per tile
+constexpr int kBN = 128;             // keys per tile of the cache
+constexpr int kBT = kMaxNodes;       // keys of the tree's tile
 constexpr int kRows = 128;           // query rows per CTA
-constexpr int kTaThreads = 192;
-constexpr int kTaWarpTma = 4, kTaWarpMma = 5;
+constexpr int kSoftmax = 256;        // threads of the softmax warps
+constexpr int kTaThreads = kSoftmax + 64;
+constexpr int kTaWarpTma = 8, kTaWarpMma = 9;
 constexpr int kTaSms = 148;          // CTAs of the launch: one per SM of the part
-constexpr int kRingBytes = 192 * 1024;
 constexpr float kRescale = 8.0f;     // log2 units
-constexpr int kMaxMTiles = kMaxNodes * 16 / kRows;
 
 __host__ __device__ inline int attn_m_tiles(int G, int T) { return (T * G + kRows - 1) / kRows; }
 __host__ __device__ inline int attn_workers(int m_tiles) { return kTaSms / m_tiles; }
@@ -147,6 +152,31 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t u) {
   return u;
 }
 
+// D[tmem] (+)= A B^T, A in tensor or shared memory, descriptors given as halves: the high half is constant for a layout
+// and the low one starts with the address / 16, so that a step costs the issuing thread one addition.
+template <bool kAccumulate>
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t desc_lo, uint32_t desc_hi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(desc_lo), "r"(desc_hi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+
+template <bool kAccumulate>
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+
 // One stretch of a worker's share within one unit.
 struct Segment {
   int n, kvh, len;   // sequence, KV head, its cache rows
@@ -180,295 +210,389 @@ struct Walk {
   }
 };
 
-// Positions in the ring, in loads since the segment's first: K_0, K_1, V_0, K_2, V_1, .. , V_{nj-1},
-// the order in which the products take them.
-__device__ __forceinline__ uint32_t ring_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
-__device__ __forceinline__ uint32_t ring_v(int j, int nj) { return j < nj - 1 ? 2 * j + 2 : 2 * nj - 1; }
+// Positions in the ring, in slots since the segment's first: K_0, K_1, V_0, K_2, V_1, .. , V_{nj-1}, two slots each, the
+// order in which the products take them; the tree's V has one slot.
+__device__ __forceinline__ uint32_t ring_k(int j) { return j == 0 ? 0 : 4 * j - 2; }
+__device__ __forceinline__ uint32_t ring_v(int j, int nj) { return j < nj - 1 ? 4 * j + 4 : 4 * nj - 2; }
+
+template <int D>
+struct TaCfg {
+  static constexpr int kQBytes = kRows * D * 2;      // blocks of 64 dims x 128 rows
+  static constexpr int kSlotBytes = 64 * D * 2;
+  static constexpr int kSlots = (D == 256 ? 160 : 192) * 1024 / kSlotBytes;
+  static constexpr uint32_t kColO = 0, kColS = D;    // tensor memory
+};
+
+template <int D>
+struct TaShared {
+  uint64_t full[TaCfg<D>::kSlots], empty[TaCfg<D>::kSlots], s_full[2], p_full[2], pv_done[2], q_full, drain;
+  long long base;
+  unsigned long long bad_v;              // nodes whose values here are not all finite
+  unsigned long long mask[kMaxNodes];    // the tree of the current sequence
+  union {
+    Tree tree;                           // while the masks are formed
+    float red[2][kRows];                 // partial row maxima (at the end sums), per column half
+  };
+  uint32_t tmem;
+  int abort, seq;
+};
+
+template <int D>
+constexpr int kTaSmem = TaCfg<D>::kQBytes + TaCfg<D>::kSlots * TaCfg<D>::kSlotBytes + static_cast<int>(sizeof(TaShared<D>)) + 1023;
+static_assert(kTaSmem<256> <= 232448 && kTaSmem<128> <= 232448, "shared memory of an SM");
 
 template <int D>
 __global__ void __launch_bounds__(kTaThreads, 1)
     attention_tree_kernel(const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
                           const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
                           const __grid_constant__ TaParams p) {
-  constexpr int kTileBytes = kBN * D * 2;
-  constexpr int kStages = kRingBytes / kTileBytes;
-  constexpr uint32_t kColO = 0, kColQ = D, kColS = D + D / 2;
-  static_assert(kColS + 2 * kBN <= 512, "tensor memory columns");
+  using C = TaCfg<D>;
+  constexpr uint32_t kSlots = C::kSlots;
   extern __shared__ uint8_t ta_smem[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ta_smem) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[kStages], empty[kStages], s_full[2], p_full[2], pv_done[2], q_full, drain_b;
-  __shared__ uint32_t tmem_base_s;
-  __shared__ int abort_s;
-  __shared__ long long chunk_s[kTaThreads + 1];
-  __shared__ int seq_s;
-  __shared__ long long base_s;
-  __shared__ Tree tree;
-  __shared__ unsigned long long bad_v_s;  // nodes whose values here are not all finite
+  uint8_t* q_sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ta_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = q_sm + C::kQBytes;
+  TaShared<D>& sh = *reinterpret_cast<TaShared<D>*>(ring + kSlots * C::kSlotBytes);
   const AttnTreeParams& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int mt = blockIdx.x, worker = blockIdx.y;
 
-  const Abort ab{a.err, &abort_s};
+  const Abort ab{a.err, &sh.abort};
   if (threadIdx.x == 0) {
-    abort_s = 0;
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    sh.abort = 0;
+    for (uint32_t i = 0; i < kSlots; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], kRows);
-      mbar_init(&pv_done[b], 1);
+      mbar_init(&sh.s_full[b], 1);
+      mbar_init(&sh.p_full[b], kSoftmax);
+      mbar_init(&sh.pv_done[b], 1);
     }
-    mbar_init(&q_full, kRows);
-    mbar_init(&drain_b, 1);
+    mbar_init(&sh.q_full, kSoftmax);
+    mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
-  if (warp == kTaWarpMma) tmem_alloc<512>(&tmem_base_s);
-  const long long total = locate(a.cache_len, a.N, a.cap, a.H_kv, worker, p.workers, -1, chunk_s, &seq_s, &base_s);
+  if (warp == kTaWarpMma) tmem_alloc<512>(&sh.tmem);
+  const long long total = locate(a.cache_len, a.N, a.cap, a.H_kv, worker, p.workers, -1,
+                                 reinterpret_cast<long long*>(q_sm), &sh.seq, &sh.base);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = tmem_base_s;
-  Walk walk{a.cache_len, a.cap, a.H_kv, a.N, seq_s, base_s, share_begin(total, worker, p.workers),
+  const uint32_t tbase = sh.tmem;
+  Walk walk{a.cache_len, a.cap, a.H_kv, a.N, sh.seq, sh.base, share_begin(total, worker, p.workers),
             share_begin(total, worker + 1, p.workers)};
   Segment sg;
 
   if (warp == kTaWarpTma) {
     if (lane == 0) {
       // ------------------------------------------------ loads, in the order of use
-      uint32_t i = 0;  // loads so far
+      uint32_t st = 0, use = 0, n_loads = 0;  // slot, times round the ring
       bool ok = true;
+      // a slot's load: false once a wait has given up
+      auto load = [&](const CUtensorMap* map, int x, int boxes, int box_rows, int row, int n, int stride) -> bool {
+        if (use > 0 && !mbar_wait(&sh.empty[st], (use - 1) & 1, ab)) return false;
+        mbar_arrive_expect_tx(&sh.full[st], static_cast<uint32_t>(boxes * box_rows * 128));
+        for (int i = 0; i < boxes; ++i)
+          tma_load_3d(ring + st * C::kSlotBytes + i * stride, map, x + 64 * i, row, n, &sh.full[st]);
+        ++n_loads;
+        if (++st == kSlots) {
+          st = 0;
+          ++use;
+        }
+        return true;
+      };
       while (ok && walk.next(sg)) {
         const int x0 = sg.kvh * D;
-        for (int l = 0; l < 2 * sg.nj && ok; ++l) {
-          // load l of the segment: K_j for l = 0, 1, 3, 5, .., V_j for l = 2, 4, .. and the last
-          const bool is_k = l == 0 || ((l & 1) && l < 2 * sg.nj - 1);
-          const int j = is_k ? (l + 1) / 2 : l == 2 * sg.nj - 1 ? sg.nj - 1 : l / 2 - 1;
-          const uint32_t st = i % kStages, use = i / kStages;
-          if (use > 0 && !mbar_wait(&empty[st], (use - 1) & 1, ab)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[st], kTileBytes);
+        auto load_k = [&](int j) {
           const bool in_tree = sg.t0 + j == sg.nt - 1;
-          const CUtensorMap* map = in_tree ? (is_k ? &tm_kt : &tm_vt) : (is_k ? &tm_kc : &tm_vc);
-          const int y = in_tree ? 0 : (sg.t0 + j) * kBN;
-#pragma unroll
-          for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(ring + st * kTileBytes + kb * (kBN * 128), map, x0 + kb * 64, y, sg.n, &full[st]);
-          ++i;
+          for (int i = 0; i < 2 && ok; ++i)
+            ok = in_tree ? load(&tm_kt, x0 + i * (D / 2), D / 128, kBT, 0, sg.n, kBN * 128)
+                         : load(&tm_kc, x0 + i * (D / 2), D / 128, kBN, (sg.t0 + j) * kBN, sg.n, kBN * 128);
+        };
+        auto load_v = [&](int j) {
+          const bool in_tree = sg.t0 + j == sg.nt - 1;
+          if (in_tree) {
+            if (ok) ok = load(&tm_vt, x0, D / 64, kBT, 0, sg.n, 64 * 128);
+          } else {
+            for (int i = 0; i < 2 && ok; ++i)
+              ok = load(&tm_vc, x0, D / 64, 64, (sg.t0 + j) * kBN + 64 * i, sg.n, 64 * 128);
+          }
+        };
+        for (int j = 0; j < sg.nj; ++j) {
+          load_k(j);
+          if (j > 0) load_v(j - 1);
         }
+        load_v(sg.nj - 1);
       }
       // copies still in flight (only after an abort) land before the CTA exits
       int drain_flag = 0;
       const Abort drain{nullptr, &drain_flag};
-      for (uint32_t k = i > kStages ? i - kStages : 0; k < i; ++k) mbar_wait(&full[k % kStages], (k / kStages) & 1, drain);
+      for (uint32_t k = n_loads > kSlots ? n_loads - kSlots : 0; k < n_loads; ++k)
+        mbar_wait(&sh.full[k % kSlots], (k / kSlots) & 1, drain);
     }
   } else if (warp == kTaWarpMma) {
     if (lane == 0) {
       // ------------------------------------------------ products
-      const uint32_t idesc_s = idesc_bf16(kRows, kBN, false, false);
+      const uint32_t idesc_s = idesc_bf16(kRows, kBN, false, false), idesc_st = idesc_bf16(kRows, kBT, false, false);
       const uint32_t idesc_o = idesc_bf16(kRows, D, false, true);
-      const uint32_t ring_a = smem_u32(ring);
-      uint32_t rb = 0;  // loads before this segment
-      uint32_t gt = 0;  // tiles before this segment
+      // K-major operands: rows of 128 B, 8-row groups 1 KiB apart; V MN-major: 64-wide blocks of d 8 KiB apart
+      const uint64_t q_desc = smem_desc(smem_u32(q_sm), 16, 1024, Swz::k128);
+      const uint64_t v_desc = smem_desc(smem_u32(ring), 64 * 128, 1024, Swz::k128);
+      const uint32_t q_lo = static_cast<uint32_t>(q_desc), k_hi = static_cast<uint32_t>(q_desc >> 32);
+      const uint32_t k_lo = q_lo + C::kQBytes / 16;
+      const uint32_t v_lo = static_cast<uint32_t>(v_desc), v_hi = static_cast<uint32_t>(v_desc >> 32);
+      uint32_t st = 0, use = 0;  // the next slot to be read, times round the ring
+      uint32_t gt = 0;           // tiles before this segment
       bool ok = true;
+      auto slot_wait = [&]() { return mbar_wait(&sh.full[st], use & 1, ab); };
+      auto slot_next = [&]() {
+        umma_commit(&sh.empty[st]);
+        if (++st == kSlots) {
+          st = 0;
+          ++use;
+        }
+      };
       for (uint32_t seg = 0; ok && walk.next(sg); ++seg) {
-        if (!mbar_wait(&q_full, seg & 1, ab)) break;
+        if (!mbar_wait(&sh.q_full, seg & 1, ab)) break;
         auto issue_pv = [&](int j) -> bool {  // O += P_j V_j
-          const uint32_t t = gt + j, ld = rb + ring_v(j, sg.nj), st = ld % kStages;
-          if (!mbar_wait(&p_full[t & 1], (t >> 1) & 1, ab)) return false;
-          if (!mbar_wait(&full[st], (ld / kStages) & 1, ab)) return false;
-          tc_fence_after();
+          const uint32_t t = gt + j;
+          const int halves = sg.t0 + j == sg.nt - 1 ? 1 : 2;
+          if (!mbar_wait(&sh.p_full[t & 1], (t >> 1) & 1, ab)) return false;
+          for (int i = 0; i < halves; ++i) {
+            if (!slot_wait()) return false;
+            tc_fence_after();
+            const uint32_t pa = tbase + C::kColS + kBN * (t & 1) + 32u * i, b = v_lo + st * (C::kSlotBytes / 16);
+            if (j > 0 || i > 0) umma_ts<true>(tbase + C::kColO, pa, b, v_hi, idesc_o);
+            else umma_ts<false>(tbase + C::kColO, pa, b, v_hi, idesc_o);
 #pragma unroll
-          for (int ks = 0; ks < kBN / 16; ++ks)
-            umma_bf16_ts(tbase + kColO, tbase + kColS + kBN * (t & 1) + 8u * ks,
-                         smem_desc(ring_a + st * kTileBytes + ks * 2048u, kBN * 128, 1024, Swz::k128), idesc_o,
-                         j > 0 || ks > 0);
-          umma_commit(&pv_done[t & 1]);
-          umma_commit(&empty[st]);
+            for (int ks = 1; ks < 4; ++ks) umma_ts<true>(tbase + C::kColO, pa + 8u * ks, b + ks * 128u, v_hi, idesc_o);
+            slot_next();
+          }
+          umma_commit(&sh.pv_done[t & 1]);
           return true;
         };
         for (int j = 0; j < sg.nj; ++j) {
-          const uint32_t t = gt + j, s = t & 1, ld = rb + ring_k(j), st = ld % kStages;
-          ok = mbar_wait(&full[st], (ld / kStages) & 1, ab);
+          const uint32_t t = gt + j, s = t & 1;
+          const uint32_t idesc = sg.t0 + j == sg.nt - 1 ? idesc_st : idesc_s;
           // S buffer s held P of two tiles before: its product must have read it
-          ok = ok && (t < 2 || mbar_wait(&pv_done[s], ((t - 2) >> 1) & 1, ab));
-          if (!ok) break;
-          tc_fence_after();
+          ok = t < 2 || mbar_wait(&sh.pv_done[s], ((t - 2) >> 1) & 1, ab);
+          for (int i = 0; i < 2 && ok; ++i) {  // the two halves of the dims
+            if (!(ok = slot_wait())) break;
+            tc_fence_after();
+            const uint32_t qa = q_lo + i * (C::kQBytes / 32), b = k_lo + st * (C::kSlotBytes / 16);
+            if (i > 0) umma_ss<true>(tbase + C::kColS + kBN * s, qa, b, k_hi, idesc);
+            else umma_ss<false>(tbase + C::kColS + kBN * s, qa, b, k_hi, idesc);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            umma_bf16_ts(tbase + kColS + kBN * s, tbase + kColQ + 8u * ks,
-                         smem_desc(ring_a + st * kTileBytes + (ks >> 2) * (kBN * 128u) + (ks & 3) * 32u, 16, 1024, Swz::k128),
-                         idesc_s, ks > 0);
-          umma_commit(&s_full[s]);
-          umma_commit(&empty[st]);
+            for (int ks = 1; ks < D / 32; ++ks)
+              umma_ss<true>(tbase + C::kColS + kBN * s, qa + (ks >> 2) * (kRows * 8u) + (ks & 3) * 2u,
+                            b + (ks >> 2) * (kBN * 8u) + (ks & 3) * 2u, k_hi, idesc);
+            slot_next();
+          }
+          if (!ok) break;
+          umma_commit(&sh.s_full[s]);
           if (j >= 1 && !(ok = issue_pv(j - 1))) break;
         }
         if (ok) ok = issue_pv(sg.nj - 1);
-        rb += 2 * sg.nj;
         gt += sg.nj;
       }
-      umma_commit(&drain_b);
+      umma_commit(&sh.drain);
       int drain_flag = 0;
       const Abort drain{nullptr, &drain_flag};
-      mbar_wait(&drain_b, 0, drain);
+      mbar_wait(&sh.drain, 0, drain);
     }
   } else {
-    // ------------------------------------------------ softmax and epilogue: thread = query row
-    const int r = 32 * warp + lane, row = mt * kRows + r;
-    const int t = row / p.G;                                  // the row's node
+    // ------------------------------------------------ softmax and epilogue: thread = query row, column half hc
+    const int q4 = warp & 3, hc = warp >> 2;
+    const int r = 32 * q4 + lane, row = mt * kRows + r;
+    const int t = row / p.G;                                // the row's node
     const bool valid = row < a.T * p.G;
-    const bool warp_on = mt * kRows + 32 * warp < a.T * p.G;  // some row of this warp
-    const uint32_t trow = tmem_addr(tbase, 32 * warp, 0);
-    uint32_t rb = 0, gt = 0;
+    const bool warp_on = mt * kRows + 32 * q4 < a.T * p.G;  // some row of this warp
+    const uint32_t trow = tmem_addr(tbase, 32 * q4, 0);
+    uint32_t rb = 0, gt = 0;  // slots and tiles before this segment
     int tree_of = -1;
-    // no early exit: the warps meet at a named barrier, so after a failed wait a warp keeps its place in the
+    // the segment's Q rows into shared memory; rows past the last node's are left as they are (no row reads another's)
+    auto fetch_q = [&](const Segment& s) {
+      const int rows = min(kRows, a.T * p.G - mt * kRows);
+      for (int x = threadIdx.x; x < rows * (D / 8); x += kSoftmax) {
+        const int i = x / (D / 8), ch = x % (D / 8), gr = mt * kRows + i;
+        const bf16* src = a.q + (static_cast<long long>(s.n) * a.T + gr / p.G) * a.ld_q +
+                          static_cast<long long>(s.kvh * p.G + gr % p.G) * D + 8 * ch;
+        cp_async16(q_sm + (ch >> 3) * (kRows * 128) + sw128_off(i, ch & 7), src);
+      }
+      cp_async_commit();
+    };
+    auto publish_q = [&]() {
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.q_full);
+    };
+    // no early exit: the warps meet at named barriers, so after a failed wait a warp keeps its place in the
     // loops and only skips its tensor-memory work
-    bool ok = true;
-    for (bool first = true; walk.next(sg); first = false) {
+    bool ok = true, have = walk.next(sg);
+    if (have) {
+      fetch_q(sg);
+      publish_q();
+    }
+    for (bool first = true; have; first = false) {
       const int h = sg.kvh * p.G + row % p.G;
       const long long tok = static_cast<long long>(sg.n) * a.T + t;
-      // Q rows into tensor memory (what an idle row holds there is never used)
-      if (ok && warp_on) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (valid ? tok * a.ld_q + static_cast<long long>(h) * D : 0));
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint4 qv[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) qv[u] = valid ? src[8 * c + u] : make_uint4(0u, 0u, 0u, 0u);
-          tmem_st32(trow + kColQ + 32u * c, reinterpret_cast<const float*>(qv));
-        }
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      mbar_arrive(&q_full);
-      // the tree of this sequence, while the first tiles load
-      if (!first) named_bar_sync(1, kRows);  // all have done with the last segment's tree and bad_v_s
-      if (tree_of != sg.n) {
+      if (!first) named_bar_sync(1, kSoftmax);  // all have done with the last segment's masks, sums and bad_v
+      if (tree_of != sg.n) {  // the tree of this sequence, while the first tiles load
         tree_of = sg.n;
-        if (warp == 0) tree_load(tree, a.parent, sg.n, a.T, mt == 0 && sg.kvh == 0 && sg.t0 == 0 ? a.err : nullptr);
+        if (warp == 0) {
+          tree_load(sh.tree, a.parent, sg.n, a.T, mt == 0 && sg.kvh == 0 && sg.t0 == 0 ? a.err : nullptr);
+          sh.mask[lane] = sh.tree.mask[lane];
+          sh.mask[lane + 32] = sh.tree.mask[lane + 32];
+        }
       }
-      if (threadIdx.x == 0) bad_v_s = 0ull;
-      named_bar_sync(1, kRows);
-      const unsigned long long mask = valid ? tree.mask[t] : 0ull;
+      if (threadIdx.x == 0) sh.bad_v = 0ull;
+      named_bar_sync(1, kSoftmax);
+      const unsigned long long mask = valid ? sh.mask[t] : 0ull;
 
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;  // l: this half's partial sum
       for (int j = 0; j < sg.nj; ++j) {
         const uint32_t tl = gt + j, s = tl & 1;
         const int tile = sg.t0 + j;
         const bool in_tree = tile == sg.nt - 1;
-        ok = ok && mbar_wait_warp(&s_full[s], (tl >> 1) & 1, ab);
+        const int lim = in_tree ? 0 : sg.len - tile * kBN;  // keys of this tile in the cache
+        ok = ok && mbar_wait_warp(&sh.s_full[s], (tl >> 1) & 1, ab);
         tc_fence_after();
-        if (ok && warp_on) {
-          float sv[kBN];
-          tmem_ld32(trow + kColS + kBN * s, sv);
-          tmem_ld32(trow + kColS + kBN * s + 32u, sv + 32);
-          tmem_wait_ld();
-          if (in_tree) {
+        if (warp_on) {
+          constexpr int kHalf = kBN / 2;
+          const bool here = !(in_tree && hc == 1);  // the tree's tile has no second half
+          float sv[kHalf];
+          float mraw = -INFINITY;
+          if (here) {
+            if (ok) {
+              tmem_ld32(trow + C::kColS + kBN * s + kHalf * hc, sv);
+              tmem_ld32(trow + C::kColS + kBN * s + kHalf * hc + 32u, sv + 32);
+              tmem_wait_ld();
+            } else {
 #pragma unroll
-            for (int c = 0; c < kBN; ++c) sv[c] = (mask >> c) & 1 ? sv[c] : -INFINITY;
-          } else if ((tile + 1) * kBN > sg.len) {
-            const int lim = sg.len - tile * kBN;
+              for (int c = 0; c < kHalf; ++c) sv[c] = 0.f;
+            }
+            if (in_tree) {
 #pragma unroll
-            for (int c = 0; c < kBN; ++c) sv[c] = c < lim ? sv[c] : -INFINITY;
+              for (int c = 0; c < kHalf; ++c) sv[c] = (mask >> c) & 1 ? sv[c] : -INFINITY;
+            } else if (lim < kBN) {
+#pragma unroll
+              for (int c = 0; c < kHalf; ++c) sv[c] = kHalf * hc + c < lim ? sv[c] : -INFINITY;
+            }
+            float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+            for (int c = 4; c < kHalf; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
+            mraw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           }
-          float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-          for (int c = 4; c < kBN; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
-          const float mloc = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2e;
-          // per warp: the wait and the tensor-memory accesses are warp-collective
+          // the row's maximum from both halves; both have read their scores before either writes P over them
+          sh.red[hc][r] = mraw;
+          named_bar_sync(2 + q4, 64);
+          const float mloc = fmaxf(mraw, sh.red[hc ^ 1][r]) * p.scale_log2e;
+          named_bar_sync(2 + q4, 64);
+          // per warp (the wait and the tensor-memory accesses are warp-collective); both warps of a row see
+          // the same maxima and decide alike
           const bool grow = mloc > m + kRescale || (m == -INFINITY && mloc > -INFINITY);
           if (__any_sync(0xffffffffu, grow)) {
             const float m_new = grow ? mloc : m;
             if (j >= 1) {
-              ok = mbar_wait_warp(&pv_done[(tl - 1) & 1], ((tl - 1) >> 1) & 1, ab);
+              ok = ok && mbar_wait_warp(&sh.pv_done[(tl - 1) & 1], ((tl - 1) >> 1) & 1, ab);
               if (ok) {
                 tc_fence_after();
                 const float f = grow ? ex2(m - m_new) : 1.f;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = 0; c < D / 64; ++c) {
                   float o[32];
-                  tmem_ld32(trow + kColO + 32u * c, o);
+                  tmem_ld32(trow + C::kColO + (D / 2) * hc + 32u * c, o);
                   tmem_wait_ld();
 #pragma unroll
                   for (int e = 0; e < 32; ++e) o[e] *= f;
-                  tmem_st32(trow + kColO + 32u * c, o);
+                  tmem_st32(trow + C::kColO + (D / 2) * hc + 32u * c, o);
                 }
                 l *= f;
               }
             }
             m = m_new;
           }
-          const float m_use = m == -INFINITY ? 0.f : m;  // nothing seen yet: every score is -inf
-          uint32_t pk[kBN / 2];
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          if (here) {
+            const float m_use = m == -INFINITY ? 0.f : m;  // nothing seen yet: every score is -inf
+            uint32_t pk[kHalf / 2];
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < kBN / 2; ++c) {
-            const float p0 = ex2(fmaf(sv[2 * c], p.scale_log2e, -m_use));
-            const float p1 = ex2(fmaf(sv[2 * c + 1], p.scale_log2e, -m_use));
-            ls[c & 3] += p0 + p1;
-            pk[c] = pack_bf16x2(p0, p1);
-          }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-          if (ok) {
-            tmem_st16(trow + kColS + kBN * s, pk);
-            tmem_st16(trow + kColS + kBN * s + 16u, pk + 16);
-            tmem_wait_st();
+            for (int c = 0; c < kHalf / 2; ++c) {
+              const float p0 = ex2(fmaf(sv[2 * c], p.scale_log2e, -m_use));
+              const float p1 = ex2(fmaf(sv[2 * c + 1], p.scale_log2e, -m_use));
+              ls[c & 3] += p0 + p1;
+              pk[c] = pack_bf16x2(p0, p1);
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            if (ok) {
+              tmem_st16(trow + C::kColS + kBN * s + 32u * hc, pk);
+              tmem_st16(trow + C::kColS + kBN * s + 32u * hc + 16u, pk + 16);
+              tmem_wait_st();
+            }
           }
         }
-        if (in_tree || (tile + 1) * kBN > sg.len) {
+        if (in_tree || lim < kBN) {
           // values that some row may not see: zero them in place before the product reads the tile
-          const uint32_t ld = rb + ring_v(j, sg.nj), st = ld % kStages;
-          ok = ok && mbar_wait_warp(&full[st], (ld / kStages) & 1, ab);
-          if (ok) {
-            uint8_t* vt = ring + st * kTileBytes;
-            const int lim = in_tree ? 0 : sg.len - tile * kBN;
-            for (int x = lim * (D / 8) + threadIdx.x; x < kBN * (D / 8); x += kRows) {
+          const uint32_t ld = rb + ring_v(j, sg.nj);
+          for (int i = 0; i < (in_tree ? 1 : 2); ++i) {
+            const uint32_t st = (ld + i) % kSlots;
+            ok = ok && mbar_wait_warp(&sh.full[st], ((ld + i) / kSlots) & 1, ab);
+            if (!ok) break;
+            uint8_t* vt = ring + st * C::kSlotBytes;
+            for (int x = max(0, lim - 64 * i) * (D / 8) + threadIdx.x; x < 64 * (D / 8); x += kSoftmax) {
               const int vr = x / (D / 8), ch = x % (D / 8);
-              uint4* at = reinterpret_cast<uint4*>(vt + (ch >> 3) * (kBN * 128) + sw128_off(vr, ch & 7));
+              uint4* at = reinterpret_cast<uint4*>(vt + (ch >> 3) * (64 * 128) + sw128_off(vr, ch & 7));
               uint4 v = make_uint4(0u, 0u, 0u, 0u);
-              if (in_tree && tree.mask[vr] != 0ull) {
+              if (in_tree && sh.mask[vr] != 0ull) {
                 const uint4 u = *at;
                 v = make_uint4(finite_only(u.x), finite_only(u.y), finite_only(u.z), finite_only(u.w));
                 if (((u.x ^ v.x) | (u.y ^ v.y) | (u.z ^ v.z) | (u.w ^ v.w)) == 0u) continue;
-                atomicOr(&bad_v_s, 1ull << vr);
+                atomicOr(&sh.bad_v, 1ull << vr);
               }
               *at = v;
             }
-            fence_proxy_async_smem();
           }
+          fence_proxy_async_smem();
         }
         tc_fence_before();
-        if (ok) mbar_arrive(&p_full[s]);
+        if (ok) mbar_arrive(&sh.p_full[s]);
       }
-      rb += 2 * sg.nj;
+      const bool tree_end = sg.t0 + sg.nj == sg.nt;
+      rb += 4 * sg.nj - (tree_end ? 1 : 0);
       gt += sg.nj;
 
-      // ---- epilogue: O is complete once the last product is
-      ok = ok && mbar_wait_warp(&pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, ab);
+      // ---- every S of this segment has been read: the next one's Q may take its place, and its first S run beside
+      // the epilogue
+      Segment nx;
+      have = walk.next(nx);
+      if (have) fetch_q(nx);
+      // O is complete once the last product is
+      ok = ok && mbar_wait_warp(&sh.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, ab);
+      if (have) publish_q();
       tc_fence_after();
-      named_bar_sync(1, kRows);  // bad_v_s is complete
+      if (warp_on) sh.red[hc][r] = l;
+      named_bar_sync(1, kSoftmax);  // both halves' sums; bad_v is complete
       if (ok && warp_on) {
+        const float l_row = l + sh.red[hc ^ 1][r];
         const bool whole = sg.nj == sg.nt;
         const bool live = mask != 0ull;
-        const unsigned long long bad = bad_v_s & mask;
+        const unsigned long long bad = sh.bad_v & mask;
         const int slot = ((worker * 2 + (first ? 0 : 1)) * p.m_tiles + mt) * p.slot_rows + r;
-        const float inv_l = 1.0f / l;
-        bf16* orow = a.out + (tok * a.H_q + h) * D;
-        float* prow = p.part_o + static_cast<long long>(slot) * D;
-        if (!whole && live) p.part_ml[slot] = make_float2(m, l);
+        const float inv_l = 1.0f / l_row;
+        const int d0 = (D / 2) * hc;
+        bf16* orow = a.out + (tok * a.H_q + h) * D + d0;
+        float* prow = p.part_o + static_cast<long long>(slot) * D + d0;
+        if (!whole && live && hc == 0) p.part_ml[slot] = make_float2(m, l_row);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
           float o[32];
-          tmem_ld32(trow + kColO + 32u * c, o);
+          tmem_ld32(trow + C::kColO + d0 + 32u * c, o);
           tmem_wait_ld();
           if (valid) {
             for (unsigned long long b = bad; b; b &= b - 1) {  // a non-finite value of a node this row sees
               const int node = __ffsll(static_cast<long long>(b)) - 1;
               const uint4* src = reinterpret_cast<const uint4*>(
-                  a.v_tree + (static_cast<long long>(sg.n) * a.T + node) * a.ld_vt + sg.kvh * D + 32 * c);
+                  a.v_tree + (static_cast<long long>(sg.n) * a.T + node) * a.ld_vt + sg.kvh * D + d0 + 32 * c);
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 float x[8];
@@ -486,9 +610,9 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 for (int e = 0; e < 8; ++e) y[e] = live ? o[8 * u + e] * inv_l : 0.f;
                 if (a.g && live) {
                   float gf[8];
-                  unpack8(reinterpret_cast<const uint4*>(a.g + tok * a.ld_g + static_cast<long long>(h) * D + 32 * c)[u], gf);
+                  unpack8(reinterpret_cast<const uint4*>(a.g + tok * a.ld_g + static_cast<long long>(h) * D + d0 + 32 * c)[u], gf);
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) y[e] = y[e] / (1.0f + __expf(-gf[e]));
+                  for (int e = 0; e < 8; ++e) y[e] = __fdividef(y[e], 1.0f + __expf(-gf[e]));
                 }
                 reinterpret_cast<uint4*>(orow + 32 * c)[u] =
                     make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
@@ -503,6 +627,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         }
       }
       tc_fence_before();
+      sg = nx;
     }
   }
   tc_fence_before();
@@ -590,10 +715,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_tree_join_kernel(const
   }
 }
 
-// bf16 rows of `cols` elements, `rows` of them for each of `outer` sequences, as 64 x 64 boxes with the 128-byte
-// swizzle; rows past the sequence's last read as zeros
+// bf16 rows of `cols` elements, `rows` of them for each of `outer` sequences, as boxes of 64 columns x box_rows with the
+// 128-byte swizzle; rows past the sequence's last read as zeros
 bool encode_rows(CUtensorMap* map, const void* base, long long cols, long long rows, long long outer, long long row_el,
-                 long long outer_el) {
+                 long long outer_el, int box_rows) {
   static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -605,7 +730,7 @@ bool encode_rows(CUtensorMap* map, const void* base, long long cols, long long r
   if (!enc) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(outer)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_el) * 2, static_cast<cuuint64_t>(outer_el) * 2};
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(kBN), 1u};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -626,15 +751,14 @@ cudaError_t launch_d(const AttnTreeParams& a, cudaStream_t stream) {
   p.part_ml = reinterpret_cast<float2*>(p.part_o + slots * D);
   const long long wk = static_cast<long long>(a.H_kv) * D;
   CUtensorMap kc, vc, kt, vt;
-  if (!encode_rows(&kc, a.k_cache, wk, a.cap, a.N, wk, wk * a.cap) ||
-      !encode_rows(&vc, a.v_cache, wk, a.cap, a.N, wk, wk * a.cap) ||
-      !encode_rows(&kt, a.k_tree, wk, a.T, a.N, a.ld_kt, a.ld_kt * a.T) ||
-      !encode_rows(&vt, a.v_tree, wk, a.T, a.N, a.ld_vt, a.ld_vt * a.T))
+  if (!encode_rows(&kc, a.k_cache, wk, a.cap, a.N, wk, wk * a.cap, kBN) ||
+      !encode_rows(&vc, a.v_cache, wk, a.cap, a.N, wk, wk * a.cap, 64) ||
+      !encode_rows(&kt, a.k_tree, wk, a.T, a.N, a.ld_kt, a.ld_kt * a.T, kBT) ||
+      !encode_rows(&vt, a.v_tree, wk, a.T, a.N, a.ld_vt, a.ld_vt * a.T, kBT))
     return cudaErrorInvalidValue;
-  constexpr int smem = kRingBytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(attention_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(attention_tree_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTaSmem<D>);
   if (e != cudaSuccess) return e;
-  attention_tree_kernel<D><<<dim3(p.m_tiles, p.workers), kTaThreads, smem, stream>>>(kc, vc, kt, vt, p);
+  attention_tree_kernel<D><<<dim3(p.m_tiles, p.workers), kTaThreads, kTaSmem<D>, stream>>>(kc, vc, kt, vt, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int groups = (a.T * p.G + kJoinRows - 1) / kJoinRows;
   attention_tree_join_kernel<D><<<dim3(groups, a.H_kv, a.N), kJoinThreads, 0, stream>>>(p);
