@@ -56,8 +56,10 @@ struct TaParams {
   AttnTreeParams a;
   int G, m_tiles, workers, slot_rows;
   float scale_log2e;
-  float* part_o;    // [workers][2][m_tiles][slot_rows][D]
-  float2* part_ml;  // [workers][2][m_tiles][slot_rows]: maximum (log2 units) and sum
+  float4* part_o;   // [workers][2][m_tiles][D / 4][slot_rows]: rows side by side, as the lanes that write and read them
+  float2* part_ml;  // [workers][2][m_tiles][slot_rows]: maximum (log2 units) and sum; an absent node's: -inf, 0
+  int4* cut;        // [workers]: the unit that begins in a worker's share and ends in a later one's: sequence
+                    // (-1: none), KV head, which of the worker's partials, the last worker
 };
 
 // tiles of one unit of sequence n: 0 when its length is out of range
@@ -76,11 +78,11 @@ __device__ __forceinline__ int share_owner(long long total, long long x, int wor
   return static_cast<int>(x < r * (q + 1) ? x / (q + 1) : r + (x - r * (q + 1)) / q);
 }
 
-// Where tile `x` of all lies: sums the units' tiles over the sequences.  Every thread of the block calls it;
+// Where worker w's share begins: sums the units' tiles over the sequences.  Every thread of the block calls it;
 // `chunk_s` has room for blockDim.x + 1 sums.  Returns the total number of tiles; *seq, *base: the sequence and the
-// tile number its first unit begins at (seq = N past the end).  With want_seq >= 0 it finds that sequence's base instead.
-__device__ long long locate(const int* cache_len, int N, int cap, int H_kv, int w, int workers, int want_seq,
-                            long long* chunk_s, int* seq_s, long long* base_s) {
+// tile number its first unit begins at (seq = N for an empty share).
+__device__ long long locate(const int* cache_len, int N, int cap, int H_kv, int w, int workers, long long* chunk_s,
+                            int* seq_s, long long* base_s) {
   const int tid = threadIdx.x, n_thr = blockDim.x;
   const int per = (N + n_thr - 1) / n_thr;
   const int n0 = min(N, tid * per), n1 = min(N, n0 + per);
@@ -112,11 +114,11 @@ __device__ long long locate(const int* cache_len, int N, int cap, int H_kv, int 
   }
   __syncthreads();
   const long long total = chunk_s[n_thr];
-  const long long x = want_seq < 0 ? share_begin(total, w, workers) : 0;
+  const long long x = share_begin(total, w, workers);
   long long at = chunk_s[tid];
   for (int n = n0; n < n1; ++n) {
     const long long next = at + static_cast<long long>(unit_tiles(cache_len[n], cap)) * H_kv;
-    if (want_seq < 0 ? (at <= x && x < next) : n == want_seq) {
+    if (at <= x && x < next) {
       *seq_s = n;
       *base_s = at;
     }
@@ -226,7 +228,7 @@ struct TaCfg {
 template <int D>
 struct TaShared {
   uint64_t full[TaCfg<D>::kSlots], empty[TaCfg<D>::kSlots], s_full[2], p_full[2], pv_done[2], q_full, drain;
-  long long base;
+  long long base, total;
   unsigned long long bad_v;              // nodes whose values here are not all finite
   unsigned long long mask[kMaxNodes];    // the tree of the current sequence
   union {
@@ -257,6 +259,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   const int mt = blockIdx.x, worker = blockIdx.y;
 
   const Abort ab{a.err, &sh.abort};
+  if (threadIdx.x == 32 * kTaWarpTma) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_kc) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_vc) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_kt) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_vt) : "memory");
+  }
   if (threadIdx.x == 0) {
     sh.abort = 0;
     for (uint32_t i = 0; i < kSlots; ++i) {
@@ -273,12 +281,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     fence_mbar_init();
   }
   if (warp == kTaWarpMma) tmem_alloc<512>(&sh.tmem);
-  const long long total = locate(a.cache_len, a.N, a.cap, a.H_kv, worker, p.workers, -1,
+  asm volatile("griddepcontrol.launch_dependents;");  // the join may be brought up; it waits for this grid's end
+  const long long total = locate(a.cache_len, a.N, a.cap, a.H_kv, worker, p.workers,
                                  reinterpret_cast<long long*>(q_sm), &sh.seq, &sh.base);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sh.tmem;
+  if (threadIdx.x == 0) sh.total = total;  // for this thread
   Walk walk{a.cache_len, a.cap, a.H_kv, a.N, sh.seq, sh.base, share_begin(total, worker, p.workers),
             share_begin(total, worker + 1, p.workers)};
   Segment sg;
@@ -429,10 +439,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     // no early exit: the warps meet at named barriers, so after a failed wait a warp keeps its place in the
     // loops and only skips its tensor-memory work
     bool ok = true, have = walk.next(sg);
-    if (have) {
-      fetch_q(sg);
-      publish_q();
+    if (have) fetch_q(sg);
+    if (threadIdx.x == 0 && mt == 0) p.cut[worker] = make_int4(-1, 0, 0, 0);
+    // sequences whose length is out of range have no tiles: their rows are zeros
+    for (int n = worker; n < a.N && mt == 0; n += p.workers) {
+      if (unit_tiles(a.cache_len[n], a.cap) > 0) continue;
+      if (threadIdx.x == 0 && a.err) atomicOr(a.err, kDevErrCacheLen);
+      uint4* dst = reinterpret_cast<uint4*>(a.out + static_cast<long long>(n) * a.T * a.H_q * D);
+      for (int x = threadIdx.x; x < a.T * a.H_q * (D / 8); x += kSoftmax) dst[x] = make_uint4(0u, 0u, 0u, 0u);
     }
+    if (have) publish_q();
     for (bool first = true; have; first = false) {
       const int h = sg.kvh * p.G + row % p.G;
       const long long tok = static_cast<long long>(sg.n) * a.T + t;
@@ -563,9 +579,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
       // ---- every S of this segment has been read: the next one's Q may take its place, and its first S run beside
       // the epilogue
+      if (sg.t0 == 0 && !tree_end)  // the unit goes on in later shares
+        if (threadIdx.x == 0 && mt == 0) p.cut[worker] = make_int4(sg.n, sg.kvh, first ? 0 : 1, share_owner(sh.total, walk.x - 1 + (sg.nt - sg.nj), p.workers));
       Segment nx;
       have = walk.next(nx);
       if (have) fetch_q(nx);
+      const bool whole = sg.nj == sg.nt;
+      const bool live = mask != 0ull;
+      const int d0 = (D / 2) * hc;
       // O is complete once the last product is
       ok = ok && mbar_wait_warp(&sh.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, ab);
       if (have) publish_q();
@@ -574,56 +595,52 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       named_bar_sync(1, kSoftmax);  // both halves' sums; bad_v is complete
       if (ok && warp_on) {
         const float l_row = l + sh.red[hc ^ 1][r];
-        const bool whole = sg.nj == sg.nt;
-        const bool live = mask != 0ull;
         const unsigned long long bad = sh.bad_v & mask;
-        const int slot = ((worker * 2 + (first ? 0 : 1)) * p.m_tiles + mt) * p.slot_rows + r;
+        const int slot = (worker * 2 + (first ? 0 : 1)) * p.m_tiles + mt;
         const float inv_l = 1.0f / l_row;
-        const int d0 = (D / 2) * hc;
-        bf16* orow = a.out + (tok * a.H_q + h) * D + d0;
-        float* prow = p.part_o + static_cast<long long>(slot) * D + d0;
-        if (!whole && live && hc == 0) p.part_ml[slot] = make_float2(m, l_row);
+        if (!whole && valid && hc == 0) p.part_ml[slot * p.slot_rows + r] = live ? make_float2(m, l_row) : make_float2(-INFINITY, 0.f);
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           float o[32];
           tmem_ld32(trow + C::kColO + d0 + 32u * c, o);
           tmem_wait_ld();
-          if (valid) {
-            for (unsigned long long b = bad; b; b &= b - 1) {  // a non-finite value of a node this row sees
-              const int node = __ffsll(static_cast<long long>(b)) - 1;
-              const uint4* src = reinterpret_cast<const uint4*>(
-                  a.v_tree + (static_cast<long long>(sg.n) * a.T + node) * a.ld_vt + sg.kvh * D + d0 + 32 * c);
+          for (unsigned long long b = bad; b; b &= b - 1) {  // a non-finite value of a node this row sees
+            const int node = __ffsll(static_cast<long long>(b)) - 1;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                a.v_tree + (static_cast<long long>(sg.n) * a.T + node) * a.ld_vt + sg.kvh * D + d0 + 32 * c);
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                float x[8];
-                unpack8(src[u], x);
+            for (int u = 0; u < 4; ++u) {
+              float x[8];
+              unpack8(src[u], x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (!isfinite(x[e])) o[8 * u + e] += x[e];
-              }
-            }
-            if (whole) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = live ? o[8 * u + e] * inv_l : 0.f;
-                if (a.g && live) {
-                  float gf[8];
-                  unpack8(reinterpret_cast<const uint4*>(a.g + tok * a.ld_g + static_cast<long long>(h) * D + d0 + 32 * c)[u], gf);
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) y[e] = __fdividef(y[e], 1.0f + __expf(-gf[e]));
-                }
-                reinterpret_cast<uint4*>(orow + 32 * c)[u] =
-                    make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-              }
-            } else if (live) {
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                reinterpret_cast<float4*>(prow + 32 * c)[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+              for (int e = 0; e < 8; ++e)
+                if (!isfinite(x[e])) o[8 * u + e] += x[e];
             }
           }
           __syncwarp();
+          if (whole && valid) {
+            bf16* orow = a.out + (tok * a.H_q + h) * D + d0 + 32 * c;
+            const bf16* grow = a.g + tok * a.ld_g + static_cast<long long>(h) * D + d0 + 32 * c;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = live ? o[8 * u + e] * inv_l : 0.f;
+              if (a.g && live) {
+                float gf[8];
+                unpack8(reinterpret_cast<const uint4*>(grow)[u], gf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = __fdividef(y[e], 1.0f + __expf(-gf[e]));
+              }
+              reinterpret_cast<uint4*>(orow)[u] =
+                  make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+            }
+          } else if (!whole && live) {
+            float4* dst = p.part_o + (static_cast<long long>(slot) * (D / 4) + d0 / 4 + 8 * c) * p.slot_rows + r;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[static_cast<long long>(u) * p.slot_rows] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          }
         }
       }
       tc_fence_before();
@@ -636,83 +653,65 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 }
 
 // Joins the partial results of the units that were cut: o = sum_i o_i 2^{m_i - M} / sum_i l_i 2^{m_i - M} over the
-// workers i that share a unit, in their order.  CTA (row group, KV head, sequence): a warp per row, a lane D / 32
-// dims.  It also writes the zero rows of sequences whose length is out of range, and reports them.
+// workers i that share a unit, in their order, with a running maximum M.  CTA (rows and dims, worker, row tile): the unit that
+// is cut at the end of that worker's share; a thread has 4 dims of a row, kFlight partials' loads in flight.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 16;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_tree_join_kernel(const __grid_constant__ TaParams p) {
+  constexpr int kFlight = 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials and cuts are complete
   const AttnTreeParams& a = p.a;
-  __shared__ long long chunk_s[kJoinThreads + 1];
-  __shared__ int seq_s;
-  __shared__ long long base_s;
-  __shared__ Tree tree;
-  const int n = blockIdx.z, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = a.cache_len[n], nt = unit_tiles(len, a.cap);
-  constexpr int kPer = D / 32;
-  if (nt > 0) {
-    const long long total = locate(a.cache_len, a.N, a.cap, a.H_kv, 0, p.workers, n, chunk_s, &seq_s, &base_s);
-    const long long u0 = base_s + static_cast<long long>(kvh) * nt, u1 = u0 + nt;
-    const int w0 = share_owner(total, u0, p.workers), w1 = share_owner(total, u1 - 1, p.workers);
-    if (w0 == w1) return;  // one worker had the whole unit and wrote it
-    if (warp == 0) tree_load(tree, a.parent, n, a.T, nullptr);
-    __syncthreads();
-    // worker w0's piece is its first when its share begins with this unit, else its last
-    const int first0 = share_begin(total, w0, p.workers) == u0 ? 0 : 1;
-    for (int i = warp; i < kJoinRows; i += kJoinThreads / 32) {
-      const int row = blockIdx.x * kJoinRows + i;
-      if (row >= a.T * p.G) break;
-      const int t = row / p.G, h = kvh * p.G + row % p.G, mt = row / kRows, r = row % kRows;
-      const long long tok = static_cast<long long>(n) * a.T + t;
-      bf16* dst = a.out + (tok * a.H_q + h) * D + lane * kPer;
-      float y[kPer];
+  const int w0 = blockIdx.y, mt = blockIdx.z;
+  const int4 cut = p.cut[w0];
+  if (cut.x < 0) return;
+  const int rows = min(kRows, a.T * p.G - mt * kRows);
+  const int x = blockIdx.x * kJoinThreads + threadIdx.x, r = x % rows, c4 = x / rows;
+  if (c4 >= D / 4) return;
+  const int row = mt * kRows + r, h = cut.y * p.G + row % p.G, w1 = cut.w;
+  const long long tok = static_cast<long long>(cut.x) * a.T + row / p.G;
+  uint2 gate = make_uint2(0u, 0u);
+  if (a.g) gate = reinterpret_cast<const uint2*>(a.g + tok * a.ld_g + static_cast<long long>(h) * D)[c4];
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, L = 0.f;
+  for (int wb = w0; wb <= w1; wb += kFlight) {
+    float2 ml[kFlight];
+    float4 v[kFlight];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) y[e] = 0.f;
-      if (tree.mask[t] != 0ull) {
-        auto slot_of = [&](int w) { return ((w * 2 + (w == w0 ? first0 : 0)) * p.m_tiles + mt) * p.slot_rows + r; };
-        float M = -INFINITY;
-        for (int w = w0 + lane; w <= w1; w += 32) M = fmaxf(M, p.part_ml[slot_of(w)].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float L = 0.f;
-        for (int w = w0; w <= w1; ++w) {
-          const int slot = slot_of(w);
-          const float2 ml = p.part_ml[slot];
-          const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-          const float4* src = reinterpret_cast<const float4*>(p.part_o + static_cast<long long>(slot) * D + lane * kPer);
-          L = fmaf(ml.y, f, L);
-#pragma unroll
-          for (int e = 0; e < kPer / 4; ++e) {
-            const float4 v = src[e];
-            y[4 * e] = fmaf(v.x, f, y[4 * e]);
-            y[4 * e + 1] = fmaf(v.y, f, y[4 * e + 1]);
-            y[4 * e + 2] = fmaf(v.z, f, y[4 * e + 2]);
-            y[4 * e + 3] = fmaf(v.w, f, y[4 * e + 3]);
-          }
-        }
-        const float inv = 1.0f / L;
-        const bf16* g = a.g ? a.g + tok * a.ld_g + static_cast<long long>(h) * D + lane * kPer : nullptr;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          y[e] *= inv;
-          if (g) y[e] = y[e] / (1.0f + __expf(-__bfloat162float(g[e])));
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < kPer; e += 4)
-        *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]));
+    for (int i = 0; i < kFlight; ++i) {
+      // worker w0's piece is its last (or only) one, the others' are their first
+      const int w = min(wb + i, w1), slot = (w * 2 + (w == w0 ? cut.z : 0)) * p.m_tiles + mt;
+      ml[i] = p.part_ml[slot * p.slot_rows + r];
+      v[i] = p.part_o[(static_cast<long long>(slot) * (D / 4) + c4) * p.slot_rows + r];
     }
-    return;
-  }
-  if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 && a.err) atomicOr(a.err, kDevErrCacheLen);
-  for (int i = warp; i < kJoinRows; i += kJoinThreads / 32) {
-    const int row = blockIdx.x * kJoinRows + i;
-    if (row >= a.T * p.G) break;
-    const long long tok = static_cast<long long>(n) * a.T + row / p.G;
-    bf16* dst = a.out + (tok * a.H_q + kvh * p.G + row % p.G) * D + lane * kPer;
+    float top = M;
 #pragma unroll
-    for (int e = 0; e < kPer; e += 4) *reinterpret_cast<uint2*>(dst + e) = make_uint2(0u, 0u);
+    for (int i = 0; i < kFlight; ++i) top = fmaxf(top, ml[i].x);
+    if (top == -INFINITY) continue;  // an absent node's row: its partials were never written
+    const float f0 = ex2(M - top);
+    M = top;
+    L *= f0;
+    y = make_float4(y.x * f0, y.y * f0, y.z * f0, y.w * f0);
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      if (wb + i > w1) break;
+      const float f = ex2(ml[i].x - M);
+      L = fmaf(ml[i].y, f, L);
+      y = make_float4(fmaf(v[i].x, f, y.x), fmaf(v[i].y, f, y.y), fmaf(v[i].z, f, y.z), fmaf(v[i].w, f, y.w));
+    }
   }
+  uint2 out = make_uint2(0u, 0u);
+  if (M > -INFINITY) {
+    const float inv = 1.0f / L;
+    float o[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+    if (a.g) {
+      o[0] = __fdividef(o[0], 1.0f + __expf(-bf16_lo(gate.x)));
+      o[1] = __fdividef(o[1], 1.0f + __expf(-bf16_hi(gate.x)));
+      o[2] = __fdividef(o[2], 1.0f + __expf(-bf16_lo(gate.y)));
+      o[3] = __fdividef(o[3], 1.0f + __expf(-bf16_hi(gate.y)));
+    }
+    out = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+  }
+  reinterpret_cast<uint2*>(a.out + (tok * a.H_q + h) * D)[c4] = out;
 }
 
 // bf16 rows of `cols` elements, `rows` of them for each of `outer` sequences, as boxes of 64 columns x box_rows with the
@@ -747,8 +746,9 @@ cudaError_t launch_d(const AttnTreeParams& a, cudaStream_t stream) {
   p.slot_rows = attn_slot_rows(p.G, a.T);
   p.scale_log2e = a.scale * 1.4426950408889634f;
   const size_t slots = static_cast<size_t>(p.workers) * 2 * p.m_tiles * p.slot_rows;
-  p.part_o = static_cast<float*>(a.workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + slots * D);
+  p.part_o = static_cast<float4*>(a.workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + slots * (D / 4));
+  p.cut = reinterpret_cast<int4*>(p.part_ml + slots);
   const long long wk = static_cast<long long>(a.H_kv) * D;
   CUtensorMap kc, vc, kt, vt;
   if (!encode_rows(&kc, a.k_cache, wk, a.cap, a.N, wk, wk * a.cap, kBN) ||
@@ -760,9 +760,17 @@ cudaError_t launch_d(const AttnTreeParams& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   attention_tree_kernel<D><<<dim3(p.m_tiles, p.workers), kTaThreads, kTaSmem<D>, stream>>>(kc, vc, kt, vt, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int groups = (a.T * p.G + kJoinRows - 1) / kJoinRows;
-  attention_tree_join_kernel<D><<<dim3(groups, a.H_kv, a.N), kJoinThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.slot_rows * (D / 4) + kJoinThreads - 1) / kJoinThreads, p.workers, p.m_tiles);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attention_tree_join_kernel<D>, p);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
@@ -770,7 +778,8 @@ cudaError_t launch_d(const AttnTreeParams& a, cudaStream_t stream) {
 size_t attention_tree_workspace(int H_q, int H_kv, int D, int, int T) {
   const int G = H_q / H_kv, m_tiles = attn_m_tiles(G, T);
   const size_t slots = static_cast<size_t>(attn_workers(m_tiles)) * 2 * m_tiles * attn_slot_rows(G, T);
-  return slots * (static_cast<size_t>(D) + 2) * sizeof(float);
+  // slots is even, so the cuts start on a 16-byte boundary
+  return slots * (static_cast<size_t>(D) + 2) * sizeof(float) + attn_workers(m_tiles) * sizeof(int4);
 }
 
 cudaError_t launch_attention_tree(const AttnTreeParams& p, cudaStream_t stream) {
