@@ -142,6 +142,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// the largest of three, NaN left out
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 __device__ __forceinline__ void unpack8(uint4 u, float* f) {
   f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
   f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
@@ -494,10 +501,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 #pragma unroll
               for (int c = 0; c < kHalf; ++c) sv[c] = kHalf * hc + c < lim ? sv[c] : -INFINITY;
             }
-            float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+            float mx[4];
 #pragma unroll
-            for (int c = 4; c < kHalf; ++c) mx[c & 3] = fmaxf(mx[c & 3], sv[c]);
-            mraw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            for (int c = 0; c < 4; ++c) mx[c] = max3(sv[3 * c], sv[3 * c + 1], sv[3 * c + 2]);
+#pragma unroll
+            for (int c = 12; c + 1 < kHalf; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], sv[c], sv[c + 1]);
+            mraw = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           }
           // the row's maximum from both halves; both have read their scores before either writes P over them
           sh.red[hc][r] = mraw;
@@ -531,15 +540,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           if (here) {
             const float m_use = m == -INFINITY ? 0.f : m;  // nothing seen yet: every score is -inf
             uint32_t pk[kHalf / 2];
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 c2 = make_float2(p.scale_log2e, p.scale_log2e), m2 = make_float2(-m_use, -m_use);
 #pragma unroll
             for (int c = 0; c < kHalf / 2; ++c) {
-              const float p0 = ex2(fmaf(sv[2 * c], p.scale_log2e, -m_use));
-              const float p1 = ex2(fmaf(sv[2 * c + 1], p.scale_log2e, -m_use));
-              ls[c & 3] += p0 + p1;
-              pk[c] = pack_bf16x2(p0, p1);
+              const float2 x = __ffma2_rn(make_float2(sv[2 * c], sv[2 * c + 1]), c2, m2);
+              const float2 e = make_float2(ex2(x.x), ex2(x.y));
+              ls[c & 1] = __fadd2_rn(ls[c & 1], e);
+              pk[c] = pack_bf16x2(e.x, e.y);
             }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
             if (ok) {
               tmem_st16(trow + C::kColS + kBN * s + 32u * hc, pk);
               tmem_st16(trow + C::kColS + kBN * s + 32u * hc + 16u, pk + 16);
@@ -587,6 +597,12 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       const bool whole = sg.nj == sg.nt;
       const bool live = mask != 0ull;
       const int d0 = (D / 2) * hc;
+      // the gate of this row's half, 32 dims ahead of their use
+      const bool gated = whole && live && a.g != nullptr;
+      const uint4* grow = reinterpret_cast<const uint4*>(a.g + (gated ? tok * a.ld_g + static_cast<long long>(h) * D + d0 : 0));
+      uint4 gv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) gv[u] = gated ? grow[u] : make_uint4(0u, 0u, 0u, 0u);
       // O is complete once the last product is
       ok = ok && mbar_wait_warp(&sh.pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, ab);
       if (have) publish_q();
@@ -620,15 +636,15 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           __syncwarp();
           if (whole && valid) {
             bf16* orow = a.out + (tok * a.H_q + h) * D + d0 + 32 * c;
-            const bf16* grow = a.g + tok * a.ld_g + static_cast<long long>(h) * D + d0 + 32 * c;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               float y[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) y[e] = live ? o[8 * u + e] * inv_l : 0.f;
-              if (a.g && live) {
+              if (gated) {
                 float gf[8];
-                unpack8(reinterpret_cast<const uint4*>(grow)[u], gf);
+                unpack8(gv[u], gf);
+                if (c + 1 < D / 64) gv[u] = grow[4 * (c + 1) + u];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = __fdividef(y[e], 1.0f + __expf(-gf[e]));
               }
