@@ -490,41 +490,58 @@ def attention_prefill(q_hat, k, v, g, B: int, T: int, out=None, err=None):
 
 # ------------------------------------------------------------------ trees of drafted tokens
 
+# These bindings run once per layer and step on small tensors, where the host's time is the call's: pointers go
+# over as plain integers, shapes and strides are read once, and the device is switched only when it has to be.
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _run_on(device, name, *args):
     """Call entry point `name` on `device` and its current stream (which comes last)."""
-    with torch.cuda.device(device):
-        _check(getattr(load(), name)(*args, _stream()), name)
+    fn = getattr(_lib or load(), name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        raise GdnError(status, name)
 
 
 def _want(name, t, dtype, shape=None, device=None):
     """A contiguous tensor of this type (and shape) on this device, or None."""
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
-def _heads(name, t, device=None):
-    """(heads, head_dim, token stride) of a bf16 [tokens][heads][head_dim] tensor, its rows contiguous."""
-    if t.dtype != torch.bfloat16:
+def _rows(name, t, tokens, heads, dim, device):
+    """Token stride of a bf16 [tokens][heads][dim] tensor whose tokens' heads lie side by side."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bf16, not {t.dtype}")
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{name} must be [tokens][heads][head_dim] with contiguous rows")
-    if device is not None and t.device != device:
+    if shape != (tokens, heads, dim):
+        raise ValueError(f"{name} must be {(tokens, heads, dim)}, not {tuple(shape)}")
+    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
+        raise ValueError(f"{name} must have its heads side by side, not strides {stride}")
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t.shape[1], t.shape[2], (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2]))
+    return stride[0] if tokens > 1 else max(stride[0], heads * dim)
 
 
-def _want_pool(H_k, H_v, state, conv_state, what=""):
+def _want_pool(H_k, H_v, state, conv_state):
     slots, dev = state.shape[0], state.device
-    _want("state" + what, state, torch.float32, (slots, H_v, HEAD_DIM, HEAD_DIM), dev)
-    _want("conv_state" + what, conv_state, torch.bfloat16, (slots, 3, (2 * H_k + H_v) * HEAD_DIM), dev)
+    _want("state", state, torch.float32, (slots, H_v, HEAD_DIM, HEAD_DIM))
+    _want("conv_state", conv_state, torch.bfloat16, (slots, 3, (2 * H_k + H_v) * HEAD_DIM), dev)
     return slots, dev
 
 
@@ -537,10 +554,11 @@ def decode_tree(inp: GdnInputs, N: int, T: int, parent, state, conv_state, state
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
     if out is None:
-        out = torch.empty(N * T, inp.H_v, HEAD_DIM, dtype=torch.bfloat16, device=dev)
-    _want("out", out, torch.bfloat16, (N * T, inp.H_v, HEAD_DIM), dev)
-    _run_on(dev, "gdn_decode_tree", ctypes.byref(inp), N, T, _ptr(parent), _ptr(state), _ptr(conv_state),
-            _ptr(state_slot), slots, _ptr(out), _ptr(err))
+        out = torch.empty((N * T, inp.H_v, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    else:
+        _want("out", out, torch.bfloat16, (N * T, inp.H_v, HEAD_DIM), dev)
+    _run_on(dev, "gdn_decode_tree", inp, N, T, _addr(parent), _addr(state), _addr(conv_state),
+            _addr(state_slot), slots, _addr(out), _addr(err))
     return out
 
 
@@ -549,15 +567,19 @@ def decode_tree_commit(inp: GdnInputs, N: int, T: int, parent, accepted, state, 
     """gdn_decode_tree_commit: state and conv_state advanced along each sequence's path to node accepted[n]
     (device int32 [N], -1: none), in place unless state_out / conv_out are given.  Returns both."""
     slots, dev = _want_pool(inp.H_k, inp.H_v, state, conv_state)
-    state_out = state if state_out is None else state_out
-    conv_out = conv_state if conv_out is None else conv_out
-    if _want_pool(inp.H_k, inp.H_v, state_out, conv_out, "_out") != (slots, dev):
-        raise ValueError("state_out must have the slots of state, on its device")
+    if state_out is None:
+        state_out = state
+    else:
+        _want("state_out", state_out, torch.float32, state.shape, dev)
+    if conv_out is None:
+        conv_out = conv_state
+    else:
+        _want("conv_out", conv_out, torch.bfloat16, conv_state.shape, dev)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("accepted", accepted, torch.int32, (N,), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
-    _run_on(dev, "gdn_decode_tree_commit", ctypes.byref(inp), N, T, _ptr(parent), _ptr(accepted), _ptr(state),
-            _ptr(state_out), _ptr(conv_state), _ptr(conv_out), _ptr(state_slot), slots, _ptr(err))
+    _run_on(dev, "gdn_decode_tree_commit", inp, N, T, _addr(parent), _addr(accepted), _addr(state),
+            _addr(state_out), _addr(conv_state), _addr(conv_out), _addr(state_slot), slots, _addr(err))
     return state_out, conv_out
 
 
@@ -582,58 +604,42 @@ def qk_norm_rope(rope: GdnRope, q, k=None, v=None, *, q_norm_w=None, k_norm_w=No
     k and v stored at `rows` (device int64, negative: not stored) of k_out, v_out [n_rows][H_kv][D].
     Returns (q_out, k_out, v_out)."""
     lead = q if q is not None else k
-    if lead is None:
-        raise ValueError("q or k is needed")
+    if lead is None or lead.dim() != 3:
+        raise ValueError("q or k is needed, [tokens][heads][head_dim]")
     dev, n_tok, D = lead.device, lead.shape[0], rope.head_dim
-    H_q = H_kv = 0
-    ld = dict.fromkeys(("q", "k", "v", "q_out", "k_out", "v_out"), 0)
-    if v is not None and k is None:
+    H_q = H_kv = n_rows = ld_q = ld_k = ld_v = ld_qo = ld_ko = ld_vo = 0
+    if q is not None:
+        H_q = q.shape[1]
+        ld_q = _rows("q", q, n_tok, H_q, D, dev)
+        if q_out is None:
+            q_out, ld_qo = torch.empty((n_tok, H_q, D), dtype=torch.bfloat16, device=dev), H_q * D
+        else:
+            ld_qo = _rows("q_out", q_out, n_tok, H_q, D, dev)
+    if k is not None:
+        H_kv = k.shape[1]
+        ld_k = _rows("k", k, n_tok, H_kv, D, dev)
+        if rows is not None and (k_out is None or (v is not None and v_out is None)):
+            raise ValueError("rows needs k_out and v_out")
+        if k_out is None:
+            k_out = torch.empty((n_tok, H_kv, D), dtype=torch.bfloat16, device=dev)
+        n_rows = k_out.shape[0]
+        ld_ko = _rows("k_out", k_out, n_rows, H_kv, D, dev)
+        if v is not None:
+            ld_v = _rows("v", v, n_tok, H_kv, D, dev)
+            if v_out is None:
+                v_out = torch.empty((n_rows, H_kv, D), dtype=torch.bfloat16, device=dev)
+            ld_vo = _rows("v_out", v_out, n_rows, H_kv, D, dev)
+    elif v is not None:
         raise ValueError("v needs k")
-    if rows is not None and k is not None and (k_out is None or (v is not None and v_out is None)):
-        raise ValueError("rows needs k_out and v_out")
-    if q is not None and q_out is None:
-        q_out = torch.empty(n_tok, q.shape[1], D, dtype=torch.bfloat16, device=dev)
-    if k is not None and k_out is None:
-        k_out = torch.empty(n_tok, k.shape[1], D, dtype=torch.bfloat16, device=dev)
-    if v is not None and v_out is None:
-        v_out = torch.empty(n_tok, v.shape[1], D, dtype=torch.bfloat16, device=dev)
-    for name, t in (("q", q), ("q_out", q_out if q is not None else None)):
-        if t is not None:
-            H_q, d, ld[name] = _heads(name, t, dev)
-            if d != D or t.shape[0] != n_tok or H_q != q.shape[1]:
-                raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
-    for name, t in (("k", k), ("v", v), ("k_out", k_out if k is not None else None),
-                    ("v_out", v_out if v is not None else None)):
-        if t is not None:
-            H_kv, d, ld[name] = _heads(name, t, dev)
-            if d != D or H_kv != k.shape[1] or (name in ("k", "v") and t.shape[0] != n_tok):
-                raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
-    n_rows = k_out.shape[0] if k is not None else 0
-    if v is not None and v_out.shape[0] != n_rows:
-        raise ValueError("k_out and v_out must have the same rows")
-    for name, t in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w)):
-        _want(name, t, torch.bfloat16, (D,), dev)
+    _want("q_norm_w", q_norm_w, torch.bfloat16, (D,), dev)
+    _want("k_norm_w", k_norm_w, torch.bfloat16, (D,), dev)
     _want("positions", positions, torch.int32, (n_tok,), dev)
     _want("rows", rows, torch.int64, (n_tok,), dev)
-    _run_on(dev, "gdn_qk_norm_rope", ctypes.byref(rope), n_tok, H_q, H_kv, _ptr(q), ld["q"], _ptr(k), ld["k"], _ptr(v),
-            ld["v"], _ptr(q_norm_w), _ptr(k_norm_w), _ptr(positions), _ptr(rows), n_rows,
-            _ptr(q_out) if q is not None else None, ld["q_out"], _ptr(k_out) if k is not None else None, ld["k_out"],
-            _ptr(v_out) if v is not None else None, ld["v_out"], _ptr(err))
+    _run_on(dev, "gdn_qk_norm_rope", rope, n_tok, H_q, H_kv, _addr(q), ld_q, _addr(k), ld_k, _addr(v), ld_v,
+            _addr(q_norm_w), _addr(k_norm_w), _addr(positions), _addr(rows), n_rows,
+            None if q is None else q_out.data_ptr(), ld_qo, None if k is None else k_out.data_ptr(), ld_ko,
+            None if v is None else v_out.data_ptr(), ld_vo, _addr(err))
     return q_out, k_out, v_out
-
-
-def _tree_rows(N, T, D, H_kv, dev, **tensors):
-    """Token strides of the nodes' tensors [N*T][heads][D]."""
-    strides = []
-    for name, t in tensors.items():
-        if t is None:
-            strides.append(0)
-            continue
-        H, d, ld = _heads(name, t, dev)
-        if d != D or t.shape[0] != N * T or (name.endswith("_tree") and H != H_kv):
-            raise ValueError(f"{name} has the wrong shape {tuple(t.shape)}")
-        strides.append(ld)
-    return strides
 
 
 def attention_tree(q_hat, k_tree, v_tree, k_cache, v_cache, cache_len, parent=None, T: int | None = None, *, g=None,
@@ -650,17 +656,20 @@ def attention_tree(q_hat, k_tree, v_tree, k_cache, v_cache, cache_len, parent=No
     _want("v_cache", v_cache, torch.bfloat16, k_cache.shape, dev)
     _want("cache_len", cache_len, torch.int32, (N,), dev)
     _want("parent", parent, torch.int32, (N, T), dev)
-    ld_q, ld_kt, ld_vt, ld_g = _tree_rows(N, T, D, H_kv, dev, q_hat=q_hat, k_tree=k_tree, v_tree=v_tree, g=g)
-    if g is not None and g.shape[1] != H_q:
-        raise ValueError("g must have the heads of q_hat")
+    n_tok = N * T
+    ld_q = _rows("q_hat", q_hat, n_tok, H_q, D, dev)
+    ld_kt = _rows("k_tree", k_tree, n_tok, H_kv, D, dev)
+    ld_vt = _rows("v_tree", v_tree, n_tok, H_kv, D, dev)
+    ld_g = 0 if g is None else _rows("g", g, n_tok, H_q, D, dev)
     if out is None:
-        out = torch.empty(N * T, H_q * D, dtype=torch.bfloat16, device=dev)
-    _want("out", out, torch.bfloat16, (N * T, H_q * D), dev)
+        out = torch.empty((n_tok, H_q * D), dtype=torch.bfloat16, device=dev)
+    else:
+        _want("out", out, torch.bfloat16, (n_tok, H_q * D), dev)
     if workspace is None:
         workspace = torch.empty(attention_tree_workspace_size(H_q, H_kv, D, N, T), dtype=torch.uint8, device=dev)
-    _run_on(dev, "gdn_attention_tree", _ptr(q_hat), ld_q, _ptr(k_tree), ld_kt, _ptr(v_tree), ld_vt, _ptr(k_cache),
-            _ptr(v_cache), cap, _ptr(cache_len), _ptr(parent), _ptr(g), ld_g, H_q, H_kv, D,
-            D ** -0.5 if scale is None else scale, N, T, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(err))
+    _run_on(dev, "gdn_attention_tree", _addr(q_hat), ld_q, _addr(k_tree), ld_kt, _addr(v_tree), ld_vt, _addr(k_cache),
+            _addr(v_cache), cap, _addr(cache_len), _addr(parent), _addr(g), ld_g, H_q, H_kv, D,
+            D ** -0.5 if scale is None else scale, N, T, _addr(out), _addr(workspace), workspace.numel(), _addr(err))
     return out
 
 
@@ -674,15 +683,19 @@ def attn_tree_commit(k_tree, v_tree, T: int, parent, accepted, k_cache, v_cache,
     cache_len_out (default cache_len itself) becomes the new lengths.  Returns it."""
     N, cap, H_kv, D = k_cache.shape
     dev = k_cache.device
-    cache_len_out = cache_len if cache_len_out is None else cache_len_out
     _want("k_cache", k_cache, torch.bfloat16, None, dev)
     _want("v_cache", v_cache, torch.bfloat16, k_cache.shape, dev)
     _want("parent", parent, torch.int32, (N, T), dev)
-    for name, t in (("accepted", accepted), ("cache_len", cache_len), ("cache_len_out", cache_len_out)):
-        _want(name, t, torch.int32, (N,), dev)
-    ld_kt, ld_vt = _tree_rows(N, T, D, H_kv, dev, k_tree=k_tree, v_tree=v_tree)
-    _run_on(dev, "gdn_attn_tree_commit", _ptr(k_tree), ld_kt, _ptr(v_tree), ld_vt, H_kv, D, N, T, _ptr(parent),
-            _ptr(accepted), _ptr(k_cache), _ptr(v_cache), cap, _ptr(cache_len), _ptr(cache_len_out), _ptr(err))
+    _want("accepted", accepted, torch.int32, (N,), dev)
+    _want("cache_len", cache_len, torch.int32, (N,), dev)
+    if cache_len_out is None:
+        cache_len_out = cache_len
+    else:
+        _want("cache_len_out", cache_len_out, torch.int32, (N,), dev)
+    ld_kt = _rows("k_tree", k_tree, N * T, H_kv, D, dev)
+    ld_vt = _rows("v_tree", v_tree, N * T, H_kv, D, dev)
+    _run_on(dev, "gdn_attn_tree_commit", _addr(k_tree), ld_kt, _addr(v_tree), ld_vt, H_kv, D, N, T, _addr(parent),
+            _addr(accepted), _addr(k_cache), _addr(v_cache), cap, _addr(cache_len), _addr(cache_len_out), _addr(err))
     return cache_len_out
 
 
@@ -700,9 +713,9 @@ def layer_decode_tree(L: GdnLayer, N: int, T: int, parent, x, state, conv_state,
     _want("state_slot", state_slot, torch.int32, (N,), dev)
     if y is None:
         y = torch.empty(N * T, L.hidden, dtype=torch.bfloat16, device=dev)
-    _run_on(dev, "gdn_layer_decode_tree", ctypes.byref(L), N, T, _ptr(parent), _ptr(x), x.stride(0), _ptr(state),
-            _ptr(conv_state), _ptr(state_slot), slots, _ptr(y), y.stride(0), _ptr(workspace), workspace.numel(),
-            _ptr(err))
+    _run_on(dev, "gdn_layer_decode_tree", L, N, T, _addr(parent), _addr(x), x.stride(0), _addr(state),
+            _addr(conv_state), _addr(state_slot), slots, _addr(y), y.stride(0), _addr(workspace), workspace.numel(),
+            _addr(err))
     return y
 
 
@@ -714,8 +727,8 @@ def layer_tree_commit(L: GdnLayer, N: int, T: int, parent, accepted, state, conv
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("accepted", accepted, torch.int32, (N,), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
-    _run_on(dev, "gdn_layer_tree_commit", ctypes.byref(L), N, T, _ptr(parent), _ptr(accepted), _ptr(state),
-            _ptr(conv_state), _ptr(state_slot), slots, _ptr(workspace), workspace.numel(), _ptr(err))
+    _run_on(dev, "gdn_layer_tree_commit", L, N, T, _addr(parent), _addr(accepted), _addr(state),
+            _addr(conv_state), _addr(state_slot), slots, _addr(workspace), workspace.numel(), _addr(err))
 
 
 def attn_layer_tree_workspace(N: int, T: int, device):
@@ -739,8 +752,8 @@ def attn_layer_decode_tree(L: GdnAttnLayer, N: int, T: int, parent, x, k_cache, 
     _want("parent", parent, torch.int32, (N, T), dev)
     if y is None:
         y = torch.empty(N * T, L.hidden, dtype=torch.bfloat16, device=dev)
-    _run_on(dev, "gdn_attn_layer_decode_tree", ctypes.byref(L), N, T, _ptr(parent), _ptr(x), x.stride(0), _ptr(k_cache),
-            _ptr(v_cache), cap, _ptr(cache_len), _ptr(y), y.stride(0), _ptr(workspace), workspace.numel(), _ptr(err))
+    _run_on(dev, "gdn_attn_layer_decode_tree", L, N, T, _addr(parent), _addr(x), x.stride(0), _addr(k_cache),
+            _addr(v_cache), cap, _addr(cache_len), _addr(y), y.stride(0), _addr(workspace), workspace.numel(), _addr(err))
     return y
 
 
@@ -749,8 +762,8 @@ def attn_layer_tree_commit(N: int, T: int, parent, accepted, k_cache, v_cache, c
     dev, cap = _want_attn_cache(N, k_cache, v_cache, cache_len)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("accepted", accepted, torch.int32, (N,), dev)
-    _run_on(dev, "gdn_attn_layer_tree_commit", N, T, _ptr(parent), _ptr(accepted), _ptr(k_cache), _ptr(v_cache), cap,
-            _ptr(cache_len), _ptr(workspace), workspace.numel(), _ptr(err))
+    _run_on(dev, "gdn_attn_layer_tree_commit", N, T, _addr(parent), _addr(accepted), _addr(k_cache), _addr(v_cache), cap,
+            _addr(cache_len), _addr(workspace), workspace.numel(), _addr(err))
 
 
 def status_string(status: int) -> str:
