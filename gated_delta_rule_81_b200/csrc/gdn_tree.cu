@@ -87,21 +87,25 @@ __device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4]
   mma_16816(d, al, b.x, b.y);
 }
 
-// the causal conv and SiLU of 8 channels of a node: its own raw row and three before it on its path
-__device__ __forceinline__ void conv8(const uint4 (&x)[kTaps], const uint4 (&w)[4], float (&y)[8]) {
-  // w[i]: channels 2 i, 2 i + 1, four taps each
+// conv weights of channels ch .. ch + CH - 1: w[i] holds the four taps of channel i
+template <int CH>
+__device__ __forceinline__ void load_taps(const bf16* conv_w, long long ch, float4 (&w)[CH]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint4& we = w[e >> 1];
-    const uint32_t w01 = e & 1 ? we.z : we.x, w23 = e & 1 ? we.w : we.y;
-    const float wt[kTaps] = {bf16_lo(w01), bf16_hi(w01), bf16_lo(w23), bf16_hi(w23)};
-    float s = 0.f;
+  for (int i = 0; i < CH / 2; ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(conv_w + ch * kTaps)[i];
+    w[2 * i] = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+    w[2 * i + 1] = make_float4(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w));
+  }
+}
+
+// the causal conv and SiLU of CH channels of a node: x[3] its own raw row (CH / 2 words), x[0 .. 2] the three before it on its
+// path, oldest first
+template <int CH>
+__device__ __forceinline__ void conv_silu(const uint32_t (&x)[kTaps][CH / 2], const float4 (&w)[CH], float (&y)[CH]) {
 #pragma unroll
-    for (int tap = 0; tap < kTaps; ++tap) {
-      const uint32_t word = (&x[tap].x)[e >> 1];
-      s = fmaf(wt[tap], e & 1 ? bf16_hi(word) : bf16_lo(word), s);
-    }
-    y[e] = silu_fast(s);
+  for (int e = 0; e < CH; ++e) {
+    auto at = [&](int tap) { return e & 1 ? bf16_hi(x[tap][e >> 1]) : bf16_lo(x[tap][e >> 1]); };
+    y[e] = silu_fast(fmaf(w[e].w, at(3), fmaf(w[e].z, at(2), fmaf(w[e].y, at(1), w[e].x * at(0)))));
   }
 }
 
@@ -187,19 +191,20 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
     const bool is_k = lane >= 16;
     const int l = lane & 15;
     const long long ch = static_cast<long long>(kh) * kD + 8 * l + (is_k ? static_cast<long long>(p.H_k) * kD : 0);
-    uint4 cw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cw[i] = reinterpret_cast<const uint4*>(p.conv_w + ch * kTaps)[i];
+    float4 cw[8];
+    load_taps<8>(p.conv_w, ch, cw);
     const uint8_t* rows = tsm + C::kOffRaw + lane * 16;
-#pragma unroll 2
+#pragma unroll(NT >= 4 ? 2 : 1)
     for (int t = warp; t < TP; t += 8) {
       float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (t < T && tree.mask[t]) {  // the same for the whole warp
-        uint4 w[kTaps];
+        uint32_t w[kTaps][4];
 #pragma unroll
-        for (int i = 0; i < kTaps; ++i)
-          w[i] = *reinterpret_cast<const uint4*>(rows + (i < kTaps - 1 ? tap_s[t][i] : t + 3) * 512);
-        conv8(w, cw, y);
+        for (int i = 0; i < kTaps; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4*>(rows + (i < kTaps - 1 ? tap_s[t][i] : t + 3) * 512);
+          w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
+        }
+        conv_silu<8>(w, cw, y);
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
   if (warp >= 8) {
     // ------------------------------------------------ the solvers: A, P and the diagonal blocks' inverses of each value head
     constexpr int kSolve = 32 * C::kSolvers;
-    const int st = tid - kWorkers, sw = warp - 8;
+    const int sw = warp - 8;
     // byte offset of element (row t, column j) in an image: the four columns of a lane side by side, hi then lo
     auto img = [](int t, int j) { return t * C::IR + (j >> 4) * 64 + ((j & 7) >> 1) * 16 + ((j & 15) >> 3) * 4 + (j & 1) * 2; };
     auto put = [](uint8_t* at, float v) {
@@ -321,23 +326,34 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
         }
       }
       if (C::kSolvers > 1) named_bar_sync(4, kSolve); else __syncwarp();
-#pragma unroll 4
-      for (int x = st; x < TP * TP; x += kSolve) {
-        const int t = x / TP, j = x % TP;
-        const bool seen = (tree.mask[t] >> j) & 1;
-        const float2 gt = sum_s[t], gj = sum_s[j];
-        const float dec = j == t ? 1.f : __expf((gt.x - gj.x) + (gt.y - gj.y));
-        const float kk = kk_s[t * C::MR + j], qk = kk_s[(TP + t) * C::MR + j];
-        float av = beta_s[jh][t] * dec * kk;
-        if (seen) {
-          put(tsm + C::kOffP + img(t, j), dec * qk);
-          if (j < t) {
-            if (!isfinite(av)) {
-              atomicOr(&poison_s[jh], 1ull << t);
-              av = 0.f;
+      // a lane per (row t, column j): a warp takes 32 / TP rows at a time, or half a row (columns past 31 only where the
+      // row has ancestors there)
+      constexpr int kRowsAtOnce = TP < 32 ? 32 / TP : 1;
+#pragma unroll(TP < 32 ? 4 : 2)
+      for (int t0 = sw * kRowsAtOnce; t0 < TP; t0 += C::kSolvers * kRowsAtOnce) {
+        const int t = t0 + (TP < 32 ? lane / TP : 0);
+        const unsigned long long mt = tree.mask[t];
+        const float2 gt = sum_s[t];
+        const float be = beta_s[jh][t];
+#pragma unroll
+        for (int half = 0; half < (TP > 32 ? 2 : 1); ++half) {
+          if (half == 1 && (mt >> 32) == 0ull) break;
+          const int j = lane % (TP < 32 ? TP : 32) + 32 * half;
+          const float2 gj = sum_s[j];
+          const float kk = kk_s[t * C::MR + j], qk = kk_s[(TP + t) * C::MR + j];
+          const float dec = j == t ? 1.f : __expf((gt.x - gj.x) + (gt.y - gj.y));
+          const float pv = dec * qk;
+          float av = be * dec * kk;
+          if ((mt >> j) & 1) {
+            put(tsm + C::kOffP + img(t, j), pv);
+            if (j < t) {
+              if (!isfinite(av)) {
+                atomicOr(&poison_s[jh], 1ull << t);
+                av = 0.f;
+              }
+              if ((t >> 4) == (j >> 4)) d_s[(t >> 4) * 320 + (t & 15) * 20 + (j & 15)] = av;
+              else put(tsm + C::kOffM + img(t, j), -av);
             }
-            if ((t >> 4) == (j >> 4)) d_s[(t >> 4) * 320 + (t & 15) * 20 + (j & 15)] = av;
-            else put(tsm + C::kOffM + img(t, j), -av);
           }
         }
       }
@@ -377,31 +393,30 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
   for (int e = 0; e < 4; ++e) nw[e] = __bfloat162float(p.norm_w[4 * lane + e]);  // norm_w: aligned to 2 bytes only
   for (int jh = 0; jh < HP; ++jh) {
     const int h = hv0 + jh;
-    // ---- v of this warp's 16 rows: a lane takes 8 channels of one node, 16 nodes at a time
+    // ---- v of this warp's 16 rows: a lane takes 4 channels of one node, 8 nodes at a time
     {
-      const int piece = lane & 1;
-      const long long ch = 2LL * p.H_k * kD + static_cast<long long>(h) * kD + 16 * warp + 8 * piece;
-      uint4 cw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) cw[i] = reinterpret_cast<const uint4*>(p.conv_w + ch * kTaps)[i];
+      const int piece = lane & 3;
+      float4 cw[4];
+      load_taps<4>(p.conv_w, 2LL * p.H_k * kD + static_cast<long long>(h) * kD + 16 * warp + 4 * piece, cw);
       if (jh > 0) {
         cp_async_wait_all();
         __syncwarp();
       }
-      const uint8_t* rows = vraw + piece * 16;
-#pragma unroll 1
-      for (int t = lane >> 1; t < TP; t += 16) {
-        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      const uint8_t* rows = vraw + piece * 8;
+#pragma unroll(NT >= 4 ? 4 : NT)
+      for (int i8 = 0; i8 < NT; ++i8) {
+        const int t = 8 * i8 + (lane >> 2);
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
         if (t < T && tree.mask[t]) {
-          uint4 w[kTaps];
+          uint32_t w[kTaps][2];
 #pragma unroll
-          for (int i = 0; i < kTaps; ++i)
-            w[i] = *reinterpret_cast<const uint4*>(rows + (i < kTaps - 1 ? tap_s[t][i] : t + 3) * 32);
-          conv8(w, cw, y);
+          for (int i = 0; i < kTaps; ++i) {
+            const uint2 u = *reinterpret_cast<const uint2*>(rows + (i < kTaps - 1 ? tap_s[t][i] : t + 3) * 32);
+            w[i][0] = u.x; w[i][1] = u.y;
+          }
+          conv_silu<4>(w, cw, y);
         }
-        float4* dst = reinterpret_cast<float4*>(v_s + t * kVRow + 16 * warp + 8 * piece);
-        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<float4*>(v_s + t * kVRow + 16 * warp + 4 * piece) = make_float4(y[0], y[1], y[2], y[3]);
       }
       __syncwarp();  // this warp's v_s columns; its raw rows are free
       if (jh + 1 < HP) {
@@ -461,6 +476,14 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
 #pragma unroll
       for (int i = 0; i < NT; ++i) clean(acc[i], i);
     }
+    // the gate's rows this warp will norm, on their way during the products
+    uint2 zz[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = warp + 8 * i;
+      zz[i] = t < T ? *reinterpret_cast<const uint2*>(p.z + (tok0 + t) * p.sz + static_cast<long long>(h) * kD + 4 * lane)
+                    : make_uint2(0u, 0u);
+    }
     // ---- block by block: U_b^T = R_b^T T_b^T, then its part of the later blocks' R and of O
     auto split_tiles = [](const float (&m0)[4], const float (&m1)[4], bool two, uint32_t (&ah)[4], uint32_t (&al)[4]) {
       split2(m0[0], m0[1], ah[0], al[0]);
@@ -506,34 +529,30 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
       dst[8] = acc[NT + i][2];
       dst[kVRow + 8] = acc[NT + i][3];
     }
-    uint2 zz[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int t = warp + 8 * i;
-      zz[i] = t < T ? *reinterpret_cast<const uint2*>(p.z + (tok0 + t) * p.sz + static_cast<long long>(h) * kD + 4 * lane)
-                    : make_uint2(0u, 0u);
-    }
     named_bar_sync(1, kWorkers);
     // ---- gated RMS norm, a warp per node
     const unsigned long long poison = poison_s[jh];
+    float4 ov[NT];
+    float ss[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      ov[i] = *reinterpret_cast<const float4*>(v_s + (warp + 8 * i) * kVRow + 4 * lane);
+      ss[i] = fmaf(ov[i].x, ov[i].x, fmaf(ov[i].y, ov[i].y, fmaf(ov[i].z, ov[i].z, ov[i].w * ov[i].w)));
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], x);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int t = warp + 8 * i;
-      if (t >= T) break;
       const unsigned long long mask = tree.mask[t];
-      uint2 y = make_uint2(0u, 0u);
-      if (mask) {
-        const float4 ov = *reinterpret_cast<const float4*>(v_s + t * kVRow + 4 * lane);
-        float ss = fmaf(ov.x, ov.x, fmaf(ov.y, ov.y, fmaf(ov.z, ov.z, ov.w * ov.w)));
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
-        const float inv = rsqrtf(ss * (1.0f / kD) + 1e-6f);
-        float f[4] = {ov.x * inv * nw[0] * silu_fast(bf16_lo(zz[i].x)), ov.y * inv * nw[1] * silu_fast(bf16_hi(zz[i].x)),
-                      ov.z * inv * nw[2] * silu_fast(bf16_lo(zz[i].y)), ov.w * inv * nw[3] * silu_fast(bf16_hi(zz[i].y))};
-        if (poison & mask) f[0] = f[1] = f[2] = f[3] = __int_as_float(0x7fffffff);
-        y = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-      }
-      *reinterpret_cast<uint2*>(p.out + ((tok0 + t) * p.H_v + h) * kD + 4 * lane) = y;
+      const float inv = rsqrtf(ss[i] * (1.0f / kD) + 1e-6f);
+      float f[4] = {ov[i].x * inv * nw[0] * silu_fast(bf16_lo(zz[i].x)), ov[i].y * inv * nw[1] * silu_fast(bf16_hi(zz[i].x)),
+                    ov[i].z * inv * nw[2] * silu_fast(bf16_lo(zz[i].y)), ov[i].w * inv * nw[3] * silu_fast(bf16_hi(zz[i].y))};
+      if (poison & mask) f[0] = f[1] = f[2] = f[3] = __int_as_float(0x7fffffff);
+      const uint2 y = mask ? make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])) : make_uint2(0u, 0u);
+      if (t < T) *reinterpret_cast<uint2*>(p.out + ((tok0 + t) * p.H_v + h) * kD + 4 * lane) = y;
     }
     if (jh + 1 < HP) named_bar_sync(1, kWorkers);  // the next head's v overwrites o
   }
