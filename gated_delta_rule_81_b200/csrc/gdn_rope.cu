@@ -16,158 +16,178 @@ namespace gdn {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTok = 4;   // tokens per CTA at most
-constexpr int kRopeItems = 4; // heads whose loads a lane group has in flight
+constexpr int kRopeFlight = 4;  // heads whose loads a lane group has in flight
 
-__device__ __forceinline__ void unpack8(uint4 u, float* f) {
-  f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
-  f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+__device__ __forceinline__ void unpack8(uint4 u, float2 (&f)[4]) {
+  f[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x));
+  f[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
+  f[2] = make_float2(bf16_lo(u.z), bf16_hi(u.z));
+  f[3] = make_float2(bf16_lo(u.w), bf16_hi(u.w));
 }
 
-// A group of W lanes (8, 16 or 32: the power of two that holds D / 8) takes a head, lane l its dims 8l .. 8l + 7
-// (one 16-byte load).  A CTA takes `tok` tokens: its threads first form the tokens' cosines and sines in
-// shared memory, R / 2 per token shared by all heads; then the groups walk the heads, kRopeItems at a time.
+// A group of W lanes (8, 16 or 32: the power of two that holds D / 8) takes `per` heads of one token, lane l their dims
+// 8l .. 8l + 7 (one 16-byte load each).  Cosines, sines and norm weights stay in registers over the heads, so that a head
+// costs little more than its own arithmetic in packed fp32: with them fetched per head, and q, k and v told apart per
+// load, the kernel spent 180 instructions per 8 elements and was bound by issuing them (179 us for 32,768 tokens of 48 heads of
+// 128; the bytes take 123 us).  Few tokens are split into many items of few heads.
 template <int W, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ gdn_rope rope, RopeParams p, int tok) {
-  __shared__ float2 cs_s[kRopeTok][GDN_ROPE_MAX_HEAD_DIM / 2];
-  __shared__ int tree_s[kRopeTok][kMaxNodes];
-  const int tid = threadIdx.x;
-  const int D = rope.head_dim, R = rope.rotary_dim, half = R / 2;
-  const long long t0 = static_cast<long long>(blockIdx.x) * tok;
-  const int n_here = static_cast<int>(min(static_cast<long long>(tok), p.n_tok - t0));
-  if (p.tree_T > 0) {  // the parents of each token's sequence, for the walk to its root
-    for (int x = tid; x < n_here * p.tree_T; x += kRopeThreads) {
-      const int i = x / p.tree_T, j = x % p.tree_T;
-      tree_s[i][j] = p.parent ? p.parent[(t0 + i) / p.tree_T * p.tree_T + j] : j - 1;
-    }
-    __syncthreads();
-  }
-  for (int x = tid; x < n_here * half; x += kRopeThreads) {
-    const int i = x / half, f = x % half;
-    long long pos = t0 + i;
-    if (p.tree_T > 0) {
-      const int j = static_cast<int>(pos % p.tree_T);
-      pos = p.base[pos / p.tree_T];
-      // one step per ancestor; a parent that is no earlier node ends the walk
-      for (int node = j, up = tree_s[i][j]; up >= 0 && up < node; node = up, up = tree_s[i][up]) ++pos;
-    } else if (p.positions) {
-      pos = p.positions[pos];
-    }
-    const unsigned long long turn = static_cast<unsigned long long>(pos) * rope.turns[f];
-    float sn, cn;
-    sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31: in half turns
-    cs_s[i][f] = make_float2(cn * rope.amplitude, sn * rope.amplitude);
-  }
-  __syncthreads();
-
+__global__ void __launch_bounds__(kRopeThreads, 4)
+    qk_norm_rope_kernel(const __grid_constant__ gdn_rope rope, const __grid_constant__ RopeParams p, int splits, int per) {
   constexpr int kGroups = kRopeThreads / W;
-  const int grp = tid / W, l = tid % W;
-  const bool on = 8 * l < D;
-  const bool turned = 8 * l < R;
-  const int H = p.H_q + p.H_kv + (p.v ? p.H_kv : 0);
-  float wq[8], wk[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) wq[e] = wk[e] = 1.f;
-  if (on && p.q_norm_w) unpack8(reinterpret_cast<const uint4*>(p.q_norm_w)[l], wq);
-  if (on && p.k_norm_w) unpack8(reinterpret_cast<const uint4*>(p.k_norm_w)[l], wk);
-  const float inv_D = 1.0f / static_cast<float>(D);
+  __shared__ int tree_s[kGroups][kMaxNodes];
+  const int grp = threadIdx.x / W, l = threadIdx.x % W;
+  const unsigned mask = W == 32 ? 0xffffffffu : ((1u << (W & 31)) - 1u) << ((threadIdx.x & 31) / W * W);
+  const long long item = static_cast<long long>(blockIdx.x) * kGroups + grp;
+  const long long t = item / splits;
+  if (t >= p.n_tok) return;  // whole groups
+  const int D = rope.head_dim, R = rope.rotary_dim;
+  const bool on = 8 * l < D, turned = 8 * l < R;
+  long long pos = t;
+  if (p.tree_T > 0) {  // the walk to the node's root, through a copy of its sequence's parents
+    const long long n = t / p.tree_T;
+    const int node = static_cast<int>(t % p.tree_T);
+    for (int j = l; j < p.tree_T; j += W) tree_s[grp][j] = p.parent ? p.parent[n * p.tree_T + j] : j - 1;
+    pos = p.base[n];
+    __syncwarp(mask);
+    for (int at = node, up = tree_s[grp][at]; up >= 0 && up < at; at = up, up = tree_s[grp][at]) ++pos;
+  } else if (p.positions) {
+    pos = p.positions[t];
+  }
+  long long row = p.rows ? p.rows[t] : t;
+  if (row >= p.n_rows) {
+    if (l == 0 && p.H_kv > 0 && p.err) atomicOr(p.err, kDevErrBadIndex);
+    row = -1;
+  }
+
   // half layout: lanes 0 .. R/16 - 1 hold the first of each pair, the next R/16 lanes the second
   const bool first = l < R / 16;
   const int partner = !turned ? l : first ? l + R / 16 : l - R / 16;
+  // factors of this lane's dims 2 e, 2 e + 1 and of the dims they are paired with
+  float2 c2[4], s2[4];
+  {
+    // four frequencies per lane: its own pairs' (interleaved), or half of those it shares with its partner
+    const int f0 = !turned ? 0 : kInterleaved ? 4 * l : first ? 8 * l : 8 * (l - R / 16) + 4;
+    float c[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned long long turn = static_cast<unsigned long long>(pos) * rope.turns[f0 + i];
+      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: in half turns
+      c[i] *= rope.amplitude;
+      s[i] *= rope.amplitude;
+    }
+    if (kInterleaved) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c2[e] = make_float2(c[e], c[e]);
+        s2[e] = make_float2(-s[e], s[e]);
+      }
+    } else {
+      const float sign = first ? -1.f : 1.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 cm = make_float2(c[2 * e], c[2 * e + 1]), sm = make_float2(s[2 * e], s[2 * e + 1]);
+        const float2 co = make_float2(__shfl_sync(mask, cm.x, partner, W), __shfl_sync(mask, cm.y, partner, W));
+        const float2 so = make_float2(__shfl_sync(mask, sm.x, partner, W), __shfl_sync(mask, sm.y, partner, W));
+        c2[e] = first ? cm : co;
+        c2[e + 2] = first ? co : cm;
+        const float2 a = first ? sm : so, b = first ? so : sm;
+        s2[e] = make_float2(sign * a.x, sign * a.y);
+        s2[e + 2] = make_float2(sign * b.x, sign * b.y);
+      }
+    }
+    if (!turned) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c2[e] = make_float2(1.f, 1.f);
+        s2[e] = make_float2(0.f, 0.f);
+      }
+    }
+  }
+  const float inv_D = 1.0f / static_cast<float>(D);
 
-  for (int i = 0; i < n_here; ++i) {
-    const long long t = t0 + i;
-    float c8[8], s8[8];  // per dim (half) or the first four per pair (interleaved)
-    if (turned) {
-      const float4* src = reinterpret_cast<const float4*>(&cs_s[i][kInterleaved ? 4 * l : 8 * (first ? l : l - R / 16)]);
+  // heads h0 .. h1 - 1 of src (and dst), normed by w and turned
+  auto heads = [&](const bf16* src, bf16* dst, const bf16* w, int h0, int h1) {
+    float2 w2[4];
 #pragma unroll
-      for (int e = 0; e < (kInterleaved ? 2 : 4); ++e) {
-        const float4 x = src[e];
-        c8[2 * e] = x.x; s8[2 * e] = x.y; c8[2 * e + 1] = x.z; s8[2 * e + 1] = x.w;
-      }
-    }
-    long long row = p.rows ? p.rows[t] : t;
-    if (row >= p.n_rows) {
-      if (tid == 0 && p.H_kv > 0 && p.err) atomicOr(p.err, kDevErrBadIndex);
-      row = -1;
-    }
-    for (int h0 = 0; h0 < H; h0 += kRopeItems * kGroups) {
-      uint4 raw[kRopeItems];
+    for (int e = 0; e < 4; ++e) w2[e] = make_float2(1.f, 1.f);
+    if (w && on) unpack8(reinterpret_cast<const uint4*>(w)[l], w2);
+    const uint4* s4 = reinterpret_cast<const uint4*>(src) + static_cast<long long>(h0) * (D / 8) + l;
+    uint4* d4 = reinterpret_cast<uint4*>(dst) + static_cast<long long>(h0) * (D / 8) + l;
+    for (int h = h0; h < h1; h += kRopeFlight, s4 += kRopeFlight * (D / 8), d4 += kRopeFlight * (D / 8)) {
+      uint4 raw[kRopeFlight];
 #pragma unroll
-      for (int u = 0; u < kRopeItems; ++u) {
-        const int h = h0 + u * kGroups + grp;
+      for (int u = 0; u < kRopeFlight; ++u) {
         raw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (on && h < H) {
-          const bf16* src = h < p.H_q            ? p.q + t * p.ld_q + static_cast<long long>(h) * D
-                            : h < p.H_q + p.H_kv ? p.k + t * p.ld_k + static_cast<long long>(h - p.H_q) * D
-                                                 : p.v + t * p.ld_v + static_cast<long long>(h - p.H_q - p.H_kv) * D;
-          raw[u] = reinterpret_cast<const uint4*>(src)[l];
-        }
+        if (on && h + u < h1) raw[u] = __ldcs(s4 + u * (D / 8));
       }
 #pragma unroll
-      for (int u = 0; u < kRopeItems; ++u) {
-        if (h0 + u * kGroups >= H) break;  // the same for the whole CTA
-        const int h = h0 + u * kGroups + grp;
-        const bool is_q = h < p.H_q, is_v = h >= p.H_q + p.H_kv;
-        float x[8];
+      for (int u = 0; u < kRopeFlight; ++u) {
+        if (h + u >= h1) break;  // the same for the group
+        float2 x[4];
         unpack8(raw[u], x);
-        float ss = 0.f;
+        if (w) {
+          float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+          for (int e = 0; e < 4; ++e) q = __ffma2_rn(x[e], x[e], q);
+          float ss = q.x + q.y;
 #pragma unroll
-        for (int o = W / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const bool norm = is_q ? p.q_norm_w != nullptr : p.k_norm_w != nullptr;
-        const float inv = norm ? rsqrtf(fmaf(ss, inv_D, rope.eps)) : 1.f;
+          for (int o = W / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+          const float inv = rsqrtf(fmaf(ss, inv_D, rope.eps));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * (is_q ? wq[e] : wk[e]);
-        if (kInterleaved) {
-          if (turned) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = x[2 * e], b = x[2 * e + 1];
-              x[2 * e] = fmaf(a, c8[e], -(b * s8[e]));
-              x[2 * e + 1] = fmaf(b, c8[e], a * s8[e]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float other = __shfl_sync(0xffffffffu, x[e], partner, W);
-            if (turned) x[e] = first ? fmaf(x[e], c8[e], -(other * s8[e])) : fmaf(x[e], c8[e], other * s8[e]);
-          }
+          for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(__fmul2_rn(x[e], make_float2(inv, inv)), w2[e]);
         }
-        if (!on || h >= H || (!is_q && row < 0)) continue;
-        if (is_v) {
-          reinterpret_cast<uint4*>(p.v_out + row * p.ld_vo + static_cast<long long>(h - p.H_q - p.H_kv) * D)[l] = raw[u];
-        } else {
-          bf16* dst = is_q ? p.q_out + t * p.ld_qo + static_cast<long long>(h) * D
-                           : p.k_out + row * p.ld_ko + static_cast<long long>(h - p.H_q) * D;
-          reinterpret_cast<uint4*>(dst)[l] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                        pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        float2 y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 other = kInterleaved ? make_float2(x[e].y, x[e].x)
+                                            : make_float2(__shfl_sync(mask, x[e].x, partner, W), __shfl_sync(mask, x[e].y, partner, W));
+          y[e] = turned ? __ffma2_rn(x[e], c2[e], __fmul2_rn(other, s2[e])) : x[e];  // (0 times an infinity left out)
         }
+        if (on)
+          d4[u * (D / 8)] = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
+                                       pack_bf16x2(y[3].x, y[3].y));
       }
     }
+  };
+  // this item's heads among q | k | v
+  const int b = static_cast<int>(item % splits) * per, e = b + per;
+  const int k0 = p.H_q, v0 = p.H_q + p.H_kv, end = v0 + (p.v ? p.H_kv : 0);
+  if (b < k0) heads(p.q + t * p.ld_q, p.q_out + t * p.ld_qo, p.q_norm_w, b, min(e, k0));
+  if (row < 0) return;
+  if (b < v0 && e > k0) heads(p.k + t * p.ld_k, p.k_out + row * p.ld_ko, p.k_norm_w, max(b, k0) - k0, min(e, v0) - k0);
+  if (e > v0 && b < end) {
+    const int h0 = max(b, v0) - v0, n16 = (min(e, end) - v0 - h0) * (D / 8);
+    const uint4* src = reinterpret_cast<const uint4*>(p.v + t * p.ld_v) + static_cast<long long>(h0) * (D / 8);
+    uint4* dst = reinterpret_cast<uint4*>(p.v_out + row * p.ld_vo) + static_cast<long long>(h0) * (D / 8);
+#pragma unroll 4
+    for (int x = l; x < n16; x += W) dst[x] = __ldcs(src + x);
   }
 }
 
 template <int W>
-void rope_launch(const gdn_rope& rope, const RopeParams& p, int tok, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((p.n_tok + tok - 1) / tok);
+void rope_launch(const gdn_rope& rope, const RopeParams& p, cudaStream_t stream) {
+  constexpr int kGroups = kRopeThreads / W;
+  const int H = p.H_q + p.H_kv + (p.v ? p.H_kv : 0);
+  // heads per item: few enough that the items fill the GPU, in rounds of kRopeFlight, and all of a token's at most
+  const long long want = 148LL * 4 * kGroups;  // groups resident at once
+  long long per = (p.n_tok * H + want - 1) / want;
+  per = (per + kRopeFlight - 1) / kRopeFlight * kRopeFlight;
+  if (per > H) per = H;
+  const int splits = static_cast<int>((H + per - 1) / per);
+  const unsigned grid = static_cast<unsigned>((p.n_tok * splits + kGroups - 1) / kGroups);
   if (rope.layout == GDN_ROPE_INTERLEAVED)
-    qk_norm_rope_kernel<W, true><<<grid, kRopeThreads, 0, stream>>>(rope, p, tok);
+    qk_norm_rope_kernel<W, true><<<grid, kRopeThreads, 0, stream>>>(rope, p, splits, static_cast<int>(per));
   else
-    qk_norm_rope_kernel<W, false><<<grid, kRopeThreads, 0, stream>>>(rope, p, tok);
+    qk_norm_rope_kernel<W, false><<<grid, kRopeThreads, 0, stream>>>(rope, p, splits, static_cast<int>(per));
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const gdn_rope& rope, const RopeParams& p, cudaStream_t stream) {
   if (p.n_tok == 0 || p.H_q + p.H_kv == 0) return cudaSuccess;
-  // several tokens per CTA share its set-up once there are CTAs enough for all SMs either way
-  const int tok = p.n_tok >= 4096 ? 4 : p.n_tok >= 1024 ? 2 : 1;
-  if (rope.head_dim <= 64) rope_launch<8>(rope, p, tok, stream);
-  else if (rope.head_dim <= 128) rope_launch<16>(rope, p, tok, stream);
-  else rope_launch<32>(rope, p, tok, stream);
+  if (rope.head_dim <= 64) rope_launch<8>(rope, p, stream);
+  else if (rope.head_dim <= 128) rope_launch<16>(rope, p, stream);
+  else rope_launch<32>(rope, p, stream);
   return cudaGetLastError();
 }
 

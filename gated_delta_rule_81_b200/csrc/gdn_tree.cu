@@ -16,7 +16,7 @@
 //   U_b = T_b (R_b - sum over blocks b' < b of A_bb' U_b'),
 // with the same number of products as a multiplication by the whole inverse, which would have to be formed row by row (a
 // dependent chain of 60 rows took 30 to 200 thousand cycles per head).  The state goes from global
-// memory straight into MMA operand registers, always four of a head's eight 16-column steps ahead, across heads; raw
+// memory straight into MMA operand registers, two of a head's eight 16-column steps ahead; raw
 // q, k and v rows come through shared memory by asynchronous copies, the next head's v during this head's products.
 //
 // The products are m16n8k16 bf16 MMAs: the state's 128 rows meet 2 T <= 128 columns once, which is too
@@ -46,7 +46,10 @@ struct TreeCfg {
   static constexpr int KT = (TP + 15) / 16;               // 16-node blocks
   static constexpr int kSolvers = NT <= 2 ? 1 : NT == 4 ? 2 : 4;
   static constexpr int kThreads = kWorkers + 32 * kSolvers;
-  static constexpr int kMinCtas = NT <= 4 ? 2 : 1;
+  // CTAs per SM: the phases of a value head are latency-bound, so warps per SM count for more than loads ahead per warp (256
+  // sequences x 8 nodes: 226 us with 4 steps ahead and 2 CTAs, 199 us with 2 and 3, 191 us with 2 and 4)
+  static constexpr int kMinCtas = NT == 1 ? 4 : NT == 2 ? 3 : NT == 4 ? 2 : 1;
+  static constexpr int kAhead = 2;                        // 16-column steps of the state loaded ahead
   static constexpr int MR = TP + 4;                       // floats of a row of the T x T products
   static constexpr int IR = KT * 64 + (KT % 2 ? 0 : 64);  // bytes of a row of an operand image
   // shared memory: [k; q] operand rows | k . k, then k . q | raw v rows | images and o, or at first raw q | k rows
@@ -118,8 +121,10 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int T = p.T, HP = p.H_v / p.H_k / parts, hv0 = (kh * parts + part) * HP;
   const long long C_conv = static_cast<long long>(2 * p.H_k + p.H_v) * kD;
-  const int slot = p.state_slot ? p.state_slot[n] : n;
   const bool leader = part == 0 && kh == 0;
+  __shared__ Tree tree;
+  if (warp == 8) tree_load(tree, p.parent, n, T, leader ? p.err : nullptr);  // (its loads beside the slot's)
+  const int slot = p.state_slot ? p.state_slot[n] : n;
   if (slot < 0 || slot >= p.n_slots) {
     if (tid == 0 && leader && p.err) atomicOr(p.err, kDevErrBadSlot);
     for (int x = tid; x < T * HP * (kD / 8); x += C::kThreads) {
@@ -132,7 +137,6 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
   float* kk_s = reinterpret_cast<float*>(tsm + C::kOffKk);
   float* d_s = reinterpret_cast<float*>(tsm + C::kOffD);
   float* v_s = reinterpret_cast<float*>(tsm + C::kOffV);
-  __shared__ Tree tree;
   __shared__ int tap_s[kMaxNodes][kTaps - 1];         // staged rows 3, 2, 1 before the node's own (t + 3) on its path
   __shared__ float g_s[kMaxHeads][TP], beta_s[kMaxHeads][TP];
   __shared__ float gamma_s[TP];
@@ -141,11 +145,11 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
 
   // ---- this warp's state rows, 16-column step ks: lane (g, c) takes columns 16 ks + 4 c .. + 3 of rows g, g + 8
   const float* S0 = p.state_in + (static_cast<long long>(slot) * p.H_v + hv0) * kD * kD;
-  float4 raw[4][2];
+  float4 raw[C::kAhead][2];
   auto load_step = [&](int jh, int ks) {
     const float* src = S0 + static_cast<long long>(jh) * kD * kD + (16 * warp + g) * kD + 16 * ks + 4 * c;
-    raw[ks & 3][0] = __ldcs(reinterpret_cast<const float4*>(src));
-    raw[ks & 3][1] = __ldcs(reinterpret_cast<const float4*>(src + 8 * kD));
+    raw[ks % C::kAhead][0] = __ldcs(reinterpret_cast<const float4*>(src));
+    raw[ks % C::kAhead][1] = __ldcs(reinterpret_cast<const float4*>(src + 8 * kD));
   };
   const bf16* hist = p.conv_in + static_cast<long long>(slot) * 3 * C_conv;
   const long long tok0 = static_cast<long long>(n) * T;
@@ -169,10 +173,9 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
   cp_async_commit();
   if (warp < 8) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) load_step(0, ks);
+    for (int ks = 0; ks < C::kAhead; ++ks) load_step(0, ks);
   }
   if (warp == 8) {
-    tree_load(tree, p.parent, n, T, leader ? p.err : nullptr);
     for (int t = lane; t < T; t += 32) {
       int at = t;
 #pragma unroll
@@ -433,16 +436,19 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
 #pragma unroll
     for (int ks = 0; ks < kD / 16; ++ks) {
       uint32_t ah[4], al[4];
-      const float4 r0 = raw[ks & 3][0], r1 = raw[ks & 3][1];
+      const float4 r0 = raw[ks % C::kAhead][0], r1 = raw[ks % C::kAhead][1];
       split2(r0.x, r0.y, ah[0], al[0]);
       split2(r1.x, r1.y, ah[1], al[1]);
       split2(r0.z, r0.w, ah[2], al[2]);
       split2(r1.z, r1.w, ah[3], al[3]);
-      if (ks < 4) load_step(jh, ks + 4);
-      else if (jh + 1 < HP) load_step(jh + 1, ks - 4);
+      if (ks < kD / 16 - C::kAhead) load_step(jh, ks + C::kAhead);
       const uint8_t* br = tsm + g * kQkRow + ks * 64 + c * 16;
 #pragma unroll
       for (int i = 0; i < 2 * NT; ++i) mma_split(acc[i], ah, al, *reinterpret_cast<const uint4*>(br + 8 * i * kQkRow));
+    }
+    if (jh + 1 < HP) {
+#pragma unroll
+      for (int ks = 0; ks < C::kAhead; ++ks) load_step(jh + 1, ks);
     }
     named_bar_sync(3, C::kThreads);  // images and gamma of this head
     // non-finite entries: their nodes are poisoned, zeros stand in

@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kCommitThreads, 2) tree_commit_kernel(TreePara
   const int H_k = p.H_k, H_v = p.H_v, G = H_v / H_k / parts, T = p.T;
   const int hv0 = (kh * parts + part) * G;
   const long long C_conv = static_cast<long long>(2 * H_k + H_v) * kD;
+  const int accepted = p.accepted[n];
   const int slot = p.state_slot ? p.state_slot[n] : n;
   if (slot < 0 || slot >= p.n_slots) {  // the same value in every thread of the cluster: its CTAs leave together
     if (tid == 0 && p.err) atomicOr(p.err, kDevErrBadSlot);
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kCommitThreads, 2) tree_commit_kernel(TreePara
   if (warp == 0) {
     int* err = part == 0 && kh == 0 ? p.err : nullptr;  // one report per sequence
     tree_load(tree, p.parent, n, T, err);
-    const unsigned long long m = tree_accepted(tree, p.accepted[n], T, err);
+    const unsigned long long m = tree_accepted(tree, accepted, T, err);
     if (lane == 0) len_s = __popcll(m);
     for (int t = lane; t < kMaxNodes; t += 32)
       if ((m >> t) & 1) path_s[__popcll(m & ((1ull << t) - 1))] = t;
@@ -260,12 +261,12 @@ __global__ void __launch_bounds__(kAppendThreads) attn_tree_commit_kernel(AttnCo
   __shared__ int path_s[kMaxNodes];
   __shared__ int len_s, base_s;
   if (tid < 32) {
+    const int accepted = p.accepted[n], base = p.cache_len[n];  // on their way beside the parents
     tree_load(tree, p.parent, n, p.T, p.err);
-    const unsigned long long m = tree_accepted(tree, p.accepted[n], p.T, p.err);
+    const unsigned long long m = tree_accepted(tree, accepted, p.T, p.err);
     for (int t = tid; t < kMaxNodes; t += 32)
       if ((m >> t) & 1) path_s[__popcll(m & ((1ull << t) - 1))] = t;
     if (tid == 0) {
-      const int base = p.cache_len[n];
       int len = __popcll(m);
       if (base < 0 || base > p.cap) {
         if (p.err) atomicOr(p.err, kDevErrCacheLen);
