@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kCommitThreads = 256;
 constexpr int kCommitPass = 8;     // path tokens per pass over the state
-constexpr int kRowsPerIter = 16;   // state rows per warp and block (8 KiB, contiguous)
+constexpr int kRowsPerIter = 8;    // state rows per warp and block (4 KiB, contiguous)
 
 __device__ __forceinline__ float4 lds4_again(const float4* p) {
   float4 v;
@@ -48,7 +48,7 @@ __host__ __device__ inline int commit_smem(int G) {
   return kCommitPass * ((n_ch - kD) * 4 + n_ch * 2) + 3 * n_ch * 2 + n_ch * kTaps * 2;
 }
 
-__global__ void __launch_bounds__(kCommitThreads, 2) tree_commit_kernel(TreeParams p) {
+__global__ void __launch_bounds__(kCommitThreads, 4) tree_commit_kernel(TreeParams p) {
   // grid (parts, H_k, N), parts CTAs of a key head in one cluster, as in decode
   const int part = blockIdx.x, parts = gridDim.x, kh = blockIdx.y, n = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -102,8 +102,7 @@ __global__ void __launch_bounds__(kCommitThreads, 2) tree_commit_kernel(TreePara
   const int len = len_s;
 
   const int g = lane >> 3, c = lane & 7;
-  const bool b2 = (c >> 2) & 1, b1 = (c >> 1) & 1;
-  const int u_me = c >> 1;
+  const int u_me = c >> 2;  // the row of its two that this lane completes
   for (int i0 = 0; i0 < len; i0 += kCommitPass) {
     const int cnt = min(kCommitPass, len - i0);
     if (i0 > 0) __syncthreads();  // the last pass has read feat and the gates
@@ -168,14 +167,15 @@ __global__ void __launch_bounds__(kCommitThreads, 2) tree_commit_kernel(TreePara
     }
     __syncthreads();
 
-    // the state rows, as in the decode kernel without its queries: a warp takes 16 contiguous rows, eight lanes
-    // share a row, and a transposed butterfly leaves lane c with s.k of row u = c >> 1 of its four
+    // the state rows, as in the decode kernel without its queries: a warp takes 8 contiguous rows, eight lanes
+    // share a row, and a transposed butterfly (the decode kernel's pairs of lanes in its order) leaves lane c with s.k of row u =
+    // c >> 2 of its two
     const float* S = i0 == 0 ? S_in : S_out;
     for (int r0 = warp * kRowsPerIter; r0 < n_rows; r0 += (kCommitThreads / 32) * kRowsPerIter) {
       const int jh = r0 >> 7;
-      float4 s[4][4];
+      float4 s[2][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int m = 0; m < 4; ++m)
           s[u][m] = __ldcs(reinterpret_cast<const float4*>(S + static_cast<long long>(r0 + g + 4 * u) * kD) + c + 8 * m);
@@ -183,45 +183,39 @@ __global__ void __launch_bounds__(kCommitThreads, 2) tree_commit_kernel(TreePara
       if (lane == 0 && r_next < n_rows) prefetch_l2(S + static_cast<long long>(r_next) * kD, kRowsPerIter * kD * 4);
       for (int t = 0; t < cnt; ++t) {
         const float4* kt = reinterpret_cast<const float4*>(feat + t * n_kv);
-        float2 ak[4];
+        float2 ak[2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) ak[u] = make_float2(0.f, 0.f);
+        for (int u = 0; u < 2; ++u) ak[u] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const float4 kk = kt[c + 8 * m];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < 2; ++u) {
             ak[u] = __ffma2_rn(make_float2(s[u][m].x, s[u][m].y), make_float2(kk.x, kk.y), ak[u]);
             ak[u] = __ffma2_rn(make_float2(s[u][m].z, s[u][m].w), make_float2(kk.z, kk.w), ak[u]);
           }
         }
-        float d[4];
+        float d[2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) d[u] = ak[u].x + ak[u].y;
-        float e[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float keep = b2 ? d[i + 2] : d[i], give = b2 ? d[i] : d[i + 2];
-          e[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
-        }
-        const float keep = b1 ? e[1] : e[0], give = b1 ? e[0] : e[1];
-        float sk = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+        for (int u = 0; u < 2; ++u) d[u] = ak[u].x + ak[u].y;
+        float sk = (u_me ? d[1] : d[0]) + __shfl_xor_sync(0xffffffffu, u_me ? d[0] : d[1], 4);
+        sk = sk + __shfl_xor_sync(0xffffffffu, sk, 2);
         sk = sk + __shfl_xor_sync(0xffffffffu, sk, 1);
         const float al = alpha_s[t * 8 + jh], be = beta_s[t * 8 + jh];
         const int r_me = r0 + g + 4 * u_me;
         const float delta_me = be * (feat[t * n_kv + kD + r_me] - al * sk);
         const float2 al2 = make_float2(al, al);
-        float2 d2[4];
+        float2 d2[2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float delta = __shfl_sync(0xffffffffu, delta_me, (lane & ~7) + 2 * u);
+        for (int u = 0; u < 2; ++u) {
+          const float delta = __shfl_sync(0xffffffffu, delta_me, (lane & ~7) + 4 * u);
           d2[u] = make_float2(delta, delta);
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const float4 kk = lds4_again(kt + c + 8 * m);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < 2; ++u) {
             const float2 lo = __ffma2_rn(al2, make_float2(s[u][m].x, s[u][m].y),
                                          __fmul2_rn(d2[u], make_float2(kk.x, kk.y)));
             const float2 hi = __ffma2_rn(al2, make_float2(s[u][m].z, s[u][m].w),
@@ -231,7 +225,7 @@ __global__ void __launch_bounds__(kCommitThreads, 2) tree_commit_kernel(TreePara
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int m = 0; m < 4; ++m)
           __stcs(reinterpret_cast<float4*>(S_out + static_cast<long long>(r0 + g + 4 * u) * kD) + c + 8 * m, s[u][m]);
