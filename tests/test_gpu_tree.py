@@ -252,6 +252,50 @@ def test_attention_tree_bad_lengths():
         assert bool((out[1] == 0).all()) and torch.equal(out[0], want[0]) and torch.equal(out[2], want[2])
 
 
+def test_attention_tree_every_length_bad():
+    c = attn_case(5, 3, 8, 2, 128, [10] * 5, "chain", seed=12)
+    c["len"].fill_(-3)
+    err = err_word()
+    out = attn_run(c, err=err)
+    assert int(err.item()) == 32 and bool((out == 0).all())
+
+
+@pytest.mark.parametrize("N,T", [(700, 1), (1300, 2)])
+def test_attention_tree_more_sequences_than_threads(N, T):
+    """The work split sums several sequences per thread; some are empty, some out of range."""
+    lens = [(i * 37) % 200 if i % 11 else 0 for i in range(N)]
+    c = attn_case(N, T, 2, 1, 128, lens, "chain", seed=N)
+    want = attn_run(c).view(N, T, -1)
+    attn_check(c, want.reshape(N * T, -1))
+    bad = torch.tensor([i for i in range(N) if i % 97 == 5], device="cuda")
+    c["len"][bad] = -1
+    err = err_word()
+    out = attn_run(c, err=err).view(N, T, -1)
+    assert int(err.item()) == 32 and bool((out[bad] == 0).all())
+    good = torch.ones(N, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    c["len"][bad] = torch.tensor([lens[int(i)] for i in bad], dtype=torch.int32, device="cuda")
+    # (another split of the work: the same sums in another order)
+    assert float((out[good].float() - want[good].float()).abs().max()) <= 4 * BF16_ULP * float(want.float().abs().max())
+
+
+def test_attention_tree_two_streams_and_rows_beside_the_output():
+    """Two calls at once on two streams, each with its own workspace and an output inside a larger buffer whose other
+    rows stay as they are."""
+    cases = [attn_case(2, 9, 24, 4, 256, [1500, 800], "holes", seed=40), attn_case(3, 20, 8, 2, 128, [700, 64, 2100], "holes", seed=41)]
+    wants = [attn_run(c) for c in cases]
+    bufs = [torch.full((w.shape[0] + 2, w.shape[1]), 5.0, dtype=torch.bfloat16, device="cuda") for w in wants]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, b, s in zip(cases, bufs, streams):
+            with torch.cuda.stream(s):
+                attn_run(c, out=b[1:-1])
+    torch.cuda.synchronize()
+    for w, b in zip(wants, bufs):
+        assert torch.equal(b[1:-1], w) and bool((b[0] == 5).all()) and bool((b[-1] == 5).all())
+
+
 def test_tree_bad_parents_are_absent_and_reported():
     c = attn_case(1, 5, 8, 2, 128, [40], "chain", seed=7)
     want = attn_run(c).view(5, -1)
@@ -363,14 +407,45 @@ def test_decode_tree(N, T, H_k, H_v, kind):
     assert torch.equal(again, out)
 
 
-def test_decode_tree_large_batch_equals_its_sequences_alone():
-    """The two launch grids (few sequences, many) give the same results within the bound."""
-    N, T, H_k, H_v = 160, 5, 1, 3
-    c = delta_case(N, T, H_k, H_v, "holes", seed=77)
-    out = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"])
-    ref = delta_ref(c)
-    t = c["there"].numpy()
-    assert out_error(out[c["there"].cuda()], ref["out"][t]) <= OUT_TOL
+@pytest.mark.parametrize("T,H_v", [(5, 3), (16, 3), (16, 8), (32, 3), (29, 8), (40, 3), (64, 2), (33, 8)])
+def test_decode_tree_large_batch(T, H_v):
+    """Many sequences: one CTA takes all the value heads of a key head in turn.  Bitwise the results of a few
+    sequences, whose value heads have a CTA each, and within the bound of the oracle."""
+    N, H_k = 150, 1
+    c = delta_case(N, T, H_k, H_v, "holes", seed=77 + T)
+    out = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"]).view(N, T, H_v, 128)
+    seqs = list(range(0, N, 29))
+    rows = torch.tensor([n * T + t for n in seqs for t in range(T)], device="cuda")
+    few = {k: c["dev"][k][rows].contiguous() for k in KEYS}
+    s = gdn.make_inputs(*(few[k] for k in ("q", "k", "v", "a", "b", "z")), c["dev"]["conv_w"], c["dev"]["A_log"], c["dev"]["norm_w"],
+                        scale=c["inp"]["scale"])
+    alone = gdn.decode_tree(s, len(seqs), T, c["parent"][seqs].contiguous(), c["d_state"], c["d_conv"],
+                            state_slot=c["d_slot"][seqs].contiguous()).view(len(seqs), T, H_v, 128)
+    assert torch.equal(alone, out[seqs])
+    sub = dict(c, rows=[c["rows"][n] for n in seqs], slot=c["slot"][seqs],
+               inp={k: v[rows.cpu()] if k in KEYS else v for k, v in c["inp"].items()})
+    there = c["there"].view(N, T)[seqs].reshape(-1)
+    ref = delta_ref(sub)["out"][there.numpy()]
+    assert out_error(alone.reshape(-1, H_v, 128)[there.cuda()], ref) <= OUT_TOL
+
+
+def test_decode_tree_and_commit_past_32_bit_offsets():
+    """A pool of more than 2^31 state elements: the sequence's slot is the last."""
+    T, H_k, H_v, slots = 9, 16, 48, 2800
+    c = delta_case(1, T, H_k, H_v, "chain", seed=3)
+    state = torch.zeros(slots, H_v, 128, 128, device="cuda")
+    assert state.numel() > 2 ** 31
+    conv = torch.zeros(slots, 3, (2 * H_k + H_v) * 128, dtype=torch.bfloat16, device="cuda")
+    state[-1], conv[-1] = c["d_state"][0], c["d_conv"][0]
+    slot = torch.tensor([slots - 1], dtype=torch.int32, device="cuda")
+    acc = torch.tensor([T - 1], dtype=torch.int32, device="cuda")
+    want = gdn.decode_tree(c["s"], 1, T, c["parent"], c["d_state"], c["d_conv"])
+    assert torch.equal(gdn.decode_tree(c["s"], 1, T, c["parent"], state, conv, state_slot=slot), want)
+    S, C = c["d_state"].clone(), c["d_conv"].clone()
+    gdn.decode_tree_commit(c["s"], 1, T, c["parent"], acc, S, C)
+    gdn.decode_tree_commit(c["s"], 1, T, c["parent"], acc, state, conv, state_slot=slot)
+    assert torch.equal(state[-1], S[0]) and torch.equal(conv[-1], C[0])
+    assert not bool(state[:-1].any()) and not bool(conv[:-1].any())
 
 
 @pytest.mark.parametrize("key", ["q", "k", "v", "a", "b", "z"])
