@@ -68,7 +68,8 @@ struct TreeCfg {
   static constexpr int kEnd = kOffV + TP * kVRow * 4;
   static constexpr int kOffRaw = kOffM;                   // [3 + TP][q 128 | k 128], until q and k are formed
   static constexpr int kRawEnd = kOffRaw + (TP + 3) * 512;
-  static constexpr int kSmem = kEnd > kRawEnd ? kEnd : kRawEnd;
+  static constexpr int kOffTaps = ((kEnd > kRawEnd ? kEnd : kRawEnd) + 15) / 16 * 16;  // conv weights of q, k and the value heads
+  static constexpr int smem(int heads) { return kOffTaps + (2 + heads) * kD * kTaps * 2; }
 };
 
 __device__ __forceinline__ void bar_arrive(int id, int n) {
@@ -95,12 +96,12 @@ __device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4]
   mma_16816(d, al, b.x, b.y);
 }
 
-// conv weights of channels ch .. ch + CH - 1: w[i] holds the four taps of channel i
+// conv weights of CH channels from their staged copy: w[i] holds the four taps of channel i
 template <int CH>
-__device__ __forceinline__ void load_taps(const bf16* conv_w, long long ch, float4 (&w)[CH]) {
+__device__ __forceinline__ void load_taps(const uint8_t* staged, float4 (&w)[CH]) {
 #pragma unroll
   for (int i = 0; i < CH / 2; ++i) {
-    const uint4 u = reinterpret_cast<const uint4*>(conv_w + ch * kTaps)[i];
+    const uint4 u = reinterpret_cast<const uint4*>(staged)[i];
     w[2 * i] = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
     w[2 * i + 1] = make_float4(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w));
   }
@@ -167,6 +168,10 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
                             : (is_k ? p.k + (tok0 + i - 3) * p.sk : p.q + (tok0 + i - 3) * p.sq) + off;
     cp_async16(tsm + C::kOffRaw + x * 16, src);
   }
+  for (int x = tid; x < (2 + HP) * 64; x += C::kThreads) {  // 64 pieces per 128 channels
+    const long long head = x < 64 ? kh : x < 128 ? p.H_k + kh : 2LL * p.H_k + hv0 + (x >> 6) - 2;
+    cp_async16(tsm + C::kOffTaps + x * 16, p.conv_w + head * kD * kTaps + (x & 63) * 8);
+  }
   uint8_t* vraw = tsm + C::kOffVraw + (warp & 7) * C::kVrawWarp;  // this worker's own
   auto stage_v = [&](int jh) {
     const long long off = static_cast<long long>(hv0 + jh) * kD + 16 * warp + 8 * (lane & 1);
@@ -198,9 +203,8 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
     // ---- q (lanes 0-15) and k (16-31) of one node per warp: conv, SiLU, norm, split into the operand rows
     const bool is_k = lane >= 16;
     const int l = lane & 15;
-    const long long ch = static_cast<long long>(kh) * kD + 8 * l + (is_k ? static_cast<long long>(p.H_k) * kD : 0);
     float4 cw[8];
-    load_taps<8>(p.conv_w, ch, cw);
+    load_taps<8>(tsm + C::kOffTaps + ((is_k ? kD : 0) + 8 * l) * kTaps * 2, cw);
     const uint8_t* rows = tsm + C::kOffRaw + lane * 16;
 #pragma unroll(NT >= 4 ? 2 : 1)
     for (int t = warp; t < TP; t += 8) {
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
     {
       const int piece = lane & 3;
       float4 cw[4];
-      load_taps<4>(p.conv_w, 2LL * p.H_k * kD + static_cast<long long>(h) * kD + 16 * warp + 4 * piece, cw);
+      load_taps<4>(tsm + C::kOffTaps + ((2 + jh) * kD + 16 * warp + 4 * piece) * kTaps * 2, cw);
       if (jh > 0) {
         cp_async_wait_all();
         __syncwarp();
@@ -572,9 +576,10 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
 template <int NT>
 cudaError_t launch_nt(const TreeParams& p, int parts, cudaStream_t stream) {
   using C = TreeCfg<NT>;
-  const cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const int smem = C::smem(p.H_v / p.H_k / parts);
+  const cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_tree_kernel<NT><<<dim3(parts, p.H_k, p.N), C::kThreads, C::kSmem, stream>>>(p);
+  decode_tree_kernel<NT><<<dim3(parts, p.H_k, p.N), C::kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
