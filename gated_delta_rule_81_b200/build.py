@@ -24,7 +24,8 @@ NVCC_FLAGS = [
 ]
 
 _GDN_SOURCES = ["gdn_api.cu", "gdn_prefill.cu", "gdn_decode.cu", "gdn_noalloc.cu", "gdn_gemm.cu", "gdn_attention.cu",
-                "gdn_tree_api.cu", "gdn_tree.cu", "gdn_tree_commit.cu", "gdn_tree_attention.cu", "gdn_rope.cu"]
+                "gdn_tree_api.cu", "gdn_tree.cu", "gdn_tree_small.cu", "gdn_tree_wide.cu",
+                "gdn_tree_commit.cu", "gdn_tree_attention.cu", "gdn_rope.cu"]
 TARGETS = {
     "libgdn.so": _GDN_SOURCES,
     "libgdn_debug.so": _GDN_SOURCES,

@@ -1,5 +1,6 @@
 // gdn_decode_tree: the delta-rule mixer's outputs of every node of a tree of drafted tokens, from
-// one read of the state.
+// one read of the state.  This file: trees of up to 32 nodes (with several value heads per CTA, of 9 to 32; gdn_tree_small.cu
+// below), the launch, and the mathematics of all three kernels; gdn_tree_wide.cu: 33 to 64 nodes.
 //
 // Per value head, with G_t the sum of the log decays on node t's path, gamma_t = e^{G_t}, D_tj = e^{G_t - G_j} for
 // an ancestor j of t (or t itself), 0 otherwise:
@@ -19,41 +20,38 @@
 // memory straight into MMA operand registers, two of a head's eight 16-column steps ahead; raw
 // q, k and v rows come through shared memory by asynchronous copies, the next head's v during this head's products.
 //
-// The products are m16n8k16 bf16 MMAs: the state's 128 rows meet 2 T <= 128 columns once, which is too
-// little per CTA for a tcgen05 tile to pay for moving the fp32 state through shared memory as bf16 pairs (built and measured: 319
-// against 329 us for 64 x 61 nodes, 175 against 134 us for 64 x 32).
+// The products are m16n8k16 bf16 MMAs: the state's 128 rows meet 2 T <= 64 columns once, which is too little per CTA for a tcgen05
+// tile to pay for moving the state through tensor memory as bf16 pairs (a tcgen05 X took 175 against 134 us for 64 sequences x 32
+// nodes; from 33 nodes on the wide kernel uses it).
 // Every operand is a pair hi + lo (hi hi + hi lo + lo hi, about 16 significant bits): the gated norm
 // amplifies the rounding of a sum whose terms nearly cancel, and plain bf16 operands leave the
 // mixer's bound.  Sums, gates and the solve are fp32, the sums of log decays fp64 (their differences over a
 // long path would lose bits).
 //
-// Measured (B200, 16 / 48 heads, the kernel alone): 256 sequences x 8 nodes 191 - 199 us (4.6 TB/s of the 906 MB it cannot do
-// without), 64 x 16 nodes 77 - 80 us, 64 x 32 134 us, 64 x 61 323 - 331 us, one sequence x 13 nodes 9 us.  Latency bounds it: a
-// warp issues every 8 to 10 cycles, so the time falls with the warps per SM, and beyond 32 nodes shared memory holds one CTA.
+// Measured (B200, 16 / 48 heads, the kernel alone): 64 sequences x 16 nodes 75 us (3.3 TB/s of the 248 MB it cannot do
+// without), 64 x 32 129 us, one sequence x 13 nodes 9 us; 256 x 8 nodes 194 us, where the small kernel takes 180.  Latency bounds it:
+// a warp issues every 8 to 10 cycles, so the time falls with the warps per SM.
 //
 // A node whose inputs are not finite: zeros stand in for its row of R and U, so that no zero weight meets an
 // infinity, and its own outputs and its descendants' become NaN; other nodes do not see it.
-#include "gdn_tree.cuh"
+#include "gdn_tree_delta.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kWorkers = 256;            // threads of warps 0-7
 constexpr int kQkRow = 576;              // bytes of one node's k (or q): 8 steps x 4 lanes x (4 hi | 4 lo), and 64 more so
                                          // that a quarter-warp's 16-byte reads of two rows fall into different banks
-constexpr int kVRow = 132;               // floats of a node's v (then o): lanes (g, c) read bank 8 c + g
-constexpr int kMaxHeads = 8;             // value heads per key head
 
 template <int NT>
 struct TreeCfg {
   static constexpr int TP = 8 * NT;                       // nodes, padded
   static constexpr int KT = (TP + 15) / 16;               // 16-node blocks
-  static constexpr int kSolvers = NT <= 2 ? 1 : NT == 4 ? 2 : 4;
+  static constexpr int kSolvers = NT <= 2 ? 1 : 2;
   static constexpr int kThreads = kWorkers + 32 * kSolvers;
   // CTAs per SM: the phases of a value head are latency-bound, so warps per SM count for more than loads ahead per warp (256
   // sequences x 8 nodes: 226 us with 4 steps ahead and 2 CTAs, 199 us with 2 and 3, 191 us with 2 and 4)
-  static constexpr int kMinCtas = NT == 1 ? 4 : NT == 2 ? 3 : NT == 4 ? 2 : 1;
+  static constexpr int kMinCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;
   static constexpr int kAhead = 2;                        // 16-column steps of the state loaded ahead
   static constexpr int MR = TP + 4;                       // floats of a row of the T x T products
   static constexpr int IR = KT * 64 + (KT % 2 ? 0 : 64);  // bytes of a row of an operand image
@@ -72,52 +70,6 @@ struct TreeCfg {
   static constexpr int smem(int heads) { return kOffTaps + (2 + heads) * kD * kTaps * 2; }
 };
 
-__device__ __forceinline__ void bar_arrive(int id, int n) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// hi and lo words of two values
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(x, y);
-  lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
-}
-
-// d += A B^T with A = ah + al and B's words b = (hi0, hi1, lo0, lo1)
-__device__ __forceinline__ void mma_split(float (&d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint4& b) {
-  mma_16816(d, ah, b.x, b.y);
-  mma_16816(d, ah, b.z, b.w);
-  mma_16816(d, al, b.x, b.y);
-}
-
-// conv weights of CH channels from their staged copy: w[i] holds the four taps of channel i
-template <int CH>
-__device__ __forceinline__ void load_taps(const uint8_t* staged, float4 (&w)[CH]) {
-#pragma unroll
-  for (int i = 0; i < CH / 2; ++i) {
-    const uint4 u = reinterpret_cast<const uint4*>(staged)[i];
-    w[2 * i] = make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-    w[2 * i + 1] = make_float4(bf16_lo(u.z), bf16_hi(u.z), bf16_lo(u.w), bf16_hi(u.w));
-  }
-}
-
-// the causal conv and SiLU of CH channels of a node: x[3] its own raw row (CH / 2 words), x[0 .. 2] the three before it on its
-// path, oldest first
-template <int CH>
-__device__ __forceinline__ void conv_silu(const uint32_t (&x)[kTaps][CH / 2], const float4 (&w)[CH], float (&y)[CH]) {
-#pragma unroll
-  for (int e = 0; e < CH; ++e) {
-    auto at = [&](int tap) { return e & 1 ? bf16_hi(x[tap][e >> 1]) : bf16_lo(x[tap][e >> 1]); };
-    y[e] = silu_fast(fmaf(w[e].w, at(3), fmaf(w[e].z, at(2), fmaf(w[e].y, at(1), w[e].x * at(0)))));
-  }
-}
-
 template <int NT>
 __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
     decode_tree_kernel(const __grid_constant__ TreeParams p) {
@@ -132,11 +84,7 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
   if (warp == 8) tree_load(tree, p.parent, n, T, leader ? p.err : nullptr);  // (its loads beside the slot's)
   const int slot = p.state_slot ? p.state_slot[n] : n;
   if (slot < 0 || slot >= p.n_slots) {
-    if (tid == 0 && leader && p.err) atomicOr(p.err, kDevErrBadSlot);
-    for (int x = tid; x < T * HP * (kD / 8); x += C::kThreads) {
-      const int t = x / (HP * (kD / 8)), y = x % (HP * (kD / 8));
-      reinterpret_cast<uint4*>(p.out + ((static_cast<long long>(n) * T + t) * p.H_v + hv0) * kD)[y] = make_uint4(0u, 0u, 0u, 0u);
-    }
+    zero_rows(p, n, T, HP, hv0, leader, tid, C::kThreads);
     return;
   }
   extern __shared__ __align__(16) uint8_t tsm[];
@@ -308,24 +256,7 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
           acc[e] = t < TP ? static_cast<double>(g_s[jh][t]) : 0.0;
           up[e] = t < T && tree.mask[t] ? tree.parent[t] : -1;
         }
-#pragma unroll 1
-        while (__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) {
-          double add[2];
-          int nu[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // the node `up` steps above, in whichever lane holds it
-            const int src = max(up[e], 0);
-            const double a0 = __shfl_sync(0xffffffffu, acc[0], src & 31), a1 = __shfl_sync(0xffffffffu, acc[1], src & 31);
-            const int u0 = __shfl_sync(0xffffffffu, up[0], src & 31), u1 = __shfl_sync(0xffffffffu, up[1], src & 31);
-            add[e] = up[e] >= 0 ? (src < 32 ? a0 : a1) : 0.0;
-            nu[e] = up[e] >= 0 ? (src < 32 ? u0 : u1) : -1;
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            acc[e] += add[e];
-            up[e] = nu[e];
-          }
-        }
+        path_sums(acc, up);
         if (jh > 0) named_bar_sync(2, C::kThreads - (kSolve - 32));  // the workers have read the last head's images
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -493,23 +424,8 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
     }
     // the gate's rows this warp will norm, on their way during the products
     uint2 zz[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int t = warp + 8 * i;
-      zz[i] = t < T ? *reinterpret_cast<const uint2*>(p.z + (tok0 + t) * p.sz + static_cast<long long>(h) * kD + 4 * lane)
-                    : make_uint2(0u, 0u);
-    }
+    load_z(zz, p, tok0, T, h, lane, warp, 8);
     // ---- block by block: U_b^T = R_b^T T_b^T, then its part of the later blocks' R and of O
-    auto split_tiles = [](const float (&m0)[4], const float (&m1)[4], bool two, uint32_t (&ah)[4], uint32_t (&al)[4]) {
-      split2(m0[0], m0[1], ah[0], al[0]);
-      split2(m0[2], m0[3], ah[1], al[1]);
-      if (two) {
-        split2(m1[0], m1[1], ah[2], al[2]);
-        split2(m1[2], m1[3], ah[3], al[3]);
-      } else {
-        ah[2] = ah[3] = al[2] = al[3] = 0u;
-      }
-    };
 #pragma unroll
     for (int b = 0; b < KT; ++b) {
       constexpr bool kTwo = NT > 1;
@@ -546,29 +462,7 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
     }
     named_bar_sync(1, kWorkers);
     // ---- gated RMS norm, a warp per node
-    const unsigned long long poison = poison_s[jh];
-    float4 ov[NT];
-    float ss[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      ov[i] = *reinterpret_cast<const float4*>(v_s + (warp + 8 * i) * kVRow + 4 * lane);
-      ss[i] = fmaf(ov[i].x, ov[i].x, fmaf(ov[i].y, ov[i].y, fmaf(ov[i].z, ov[i].z, ov[i].w * ov[i].w)));
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], x);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int t = warp + 8 * i;
-      const unsigned long long mask = tree.mask[t];
-      const float inv = rsqrtf(ss[i] * (1.0f / kD) + 1e-6f);
-      float f[4] = {ov[i].x * inv * nw[0] * silu_fast(bf16_lo(zz[i].x)), ov[i].y * inv * nw[1] * silu_fast(bf16_hi(zz[i].x)),
-                    ov[i].z * inv * nw[2] * silu_fast(bf16_lo(zz[i].y)), ov[i].w * inv * nw[3] * silu_fast(bf16_hi(zz[i].y))};
-      if (poison & mask) f[0] = f[1] = f[2] = f[3] = __int_as_float(0x7fffffff);
-      const uint2 y = mask ? make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])) : make_uint2(0u, 0u);
-      if (t < T) *reinterpret_cast<uint2*>(p.out + ((tok0 + t) * p.H_v + h) * kD + 4 * lane) = y;
-    }
+    norm_rows(zz, v_s, nw, p, tree, poison_s[jh], tok0, T, h, lane, warp, 8);
     if (jh + 1 < HP) named_bar_sync(1, kWorkers);  // the next head's v overwrites o
   }
 }
@@ -593,10 +487,13 @@ cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream, void* c
   // one CTA per value head while one per key head would leave SMs idle
   const int parts = static_cast<long long>(p.N) * p.H_k < n_sm ? p.H_v / p.H_k : 1;
   if (events) cudaEventRecord(static_cast<cudaEvent_t>(events[0]), stream);
-  e = p.T <= 8 ? launch_nt<1>(p, parts, stream)
+  // up to 8 nodes: the small kernel, unless a CTA has one value head (16 / 16 heads, 64 x 8 nodes: 28.7 against 26.5 us; 16 / 48
+  // heads, 64 x 8 nodes: 52 against 57 us, 10 x 8 17 against 19, 256 x 1 152 against 172)
+  e = p.T <= 8 && parts == 1 && p.H_v > p.H_k ? launch_decode_tree_small(p, stream)
+      : p.T <= 8 ? launch_nt<1>(p, parts, stream)
       : p.T <= 16 ? launch_nt<2>(p, parts, stream)
       : p.T <= 32 ? launch_nt<4>(p, parts, stream)
-                  : launch_nt<8>(p, parts, stream);
+                  : launch_decode_tree_wide(p, parts, stream);
   if (events) cudaEventRecord(static_cast<cudaEvent_t>(events[1]), stream);
   return e;
 }

@@ -429,6 +429,36 @@ def test_decode_tree_large_batch(T, H_v):
     assert out_error(alone.reshape(-1, H_v, 128)[there.cuda()], ref) <= OUT_TOL
 
 
+@pytest.mark.parametrize("T,H_v", [(1, 2), (8, 8), (7, 5), (4, 3), (64, 8), (61, 4), (37, 3), (33, 6)])
+def test_decode_tree_large_batch_with_bad_slots_and_nodes(T, H_v):
+    """Many sequences, several value heads per CTA: slots that are shared or out of range, a node whose key is not finite and bad
+    parents, each without effect on the other sequences, which keep bitwise the results that they have alone."""
+    N, H_k = 150, 1
+    c = delta_case(N, T, H_k, H_v, "holes", seed=177 + T)
+    slot = c["slot"].clone()
+    slot[3], slot[70], slot[149], slot[20] = N, -1, 2 ** 31 - 1, slot[21]
+    seq = 40
+    bad = int(c["there"].view(N, T)[seq].nonzero()[0])
+    c["dev"]["k"][seq * T + bad] = float("inf")
+    parent = c["parent"].clone()
+    parent[50, T - 1] = T + 5
+    err = err_word()
+    out = gdn.decode_tree(c["s"], N, T, parent, c["d_state"], c["d_conv"], state_slot=slot.cuda(), err=err).view(N, T, H_v, 128)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 8 | 128
+    assert bool((out[[3, 70, 149]] == 0).all())
+    assert bool((out[50, T - 1] == 0).all())
+    hit = torch.tensor([bad in p for p in oracle.tree.paths(c["rows"][seq])], device="cuda")
+    assert bool(torch.isnan(out[seq][hit]).all()) and not bool(torch.isnan(out[seq][~hit]).any())
+    for n in (0, 20, 21, seq, 50, 101, 148):
+        rows = torch.arange(n * T, (n + 1) * T, device="cuda")
+        one = {k: c["dev"][k][rows].contiguous() for k in KEYS}
+        s = gdn.make_inputs(*(one[k] for k in ("q", "k", "v", "a", "b", "z")), c["dev"]["conv_w"], c["dev"]["A_log"],
+                            c["dev"]["norm_w"], scale=c["inp"]["scale"])
+        alone = gdn.decode_tree(s, 1, T, parent[n:n + 1].contiguous(), c["d_state"], c["d_conv"], state_slot=slot[n:n + 1].cuda())
+        assert torch.equal(alone.view(T, H_v, 128).view(torch.int16), out[n].view(torch.int16)), n
+
+
 def test_decode_tree_and_commit_past_32_bit_offsets():
     """A pool of more than 2^31 state elements: the sequence's slot is the last."""
     T, H_k, H_v, slots = 9, 16, 48, 2800
