@@ -3,11 +3,11 @@
 // For sequence n and KV head kvh, the T nodes times the G query heads that share kvh are T G query
 // rows (row t G + g), all over the same keys: cache_len[n] cache rows, then the T nodes' own.  With
 //   s_rj = scale q_r . k_j,  m_r = max_j s_rj,  o_r = sum_j e^{s_rj - m_r} v_j / sum_j e^{s_rj - m_r}
-// over the keys row r sees, the keys are taken once, in tiles of 64, with a running maximum and sum.
+// over the keys row r sees, the keys are taken once, in tiles of 128, with a running maximum and sum.
 //
 // Work split.  A unit is one (sequence, KV head): its tiles are ceil(cache_len / 128) tiles of the cache and
-// one tile of the tree (64 keys).  The tiles of all units in a row are cut into W equal shares, one per
-// worker, so that ragged lengths balance and a single long sequence still fills the GPU; a unit cut between
+// one tile of the tree (64 keys).  The tiles of all units in a row, each unit's preceded by what its beginning and
+// end cost (kUnitCost), are cut into W equal shares, one per worker, so that ragged lengths balance and a single long sequence still fills the GPU; a unit cut between
 // workers leaves partial (o, m, l) that a second kernel joins.  Rows beyond 128 go to further CTAs (blockIdx.x)
 // of the same worker, which read the same tiles at about the same time, from L2.
 //
@@ -26,8 +26,8 @@
 //
 // Measured (B200, 24 / 4 heads of 256, kernels alone): one sequence of 262,144 keys x 64 nodes 380 - 388 us, 1.07 PFLOP/s, bound by
 // shared memory (a tile's 64 KB of Q, 64 + 64 KB of K and V read and 128 KB written take 2500 of its 3200 cycles, the products
-// 2050); 64 ragged sequences of up to 8192 keys x 16 nodes 282 us (4424 GB/s over all, HBM's rate while tiles stream), x 1 node 220
-// us (5495 GB/s); one token of 777 keys 14 us.
+// 2050); 64 ragged sequences of up to 8192 keys x 16 nodes 226 us (5510 GB/s over all, HBM's rate while tiles stream), x 1 node 197
+// us (6140 GB/s); one token of 777 keys 14 us.
 //
 // Whatever a row may not see contributes exactly nothing: masked scores become -inf by selection, so infinities
 // and NaN in masked keys vanish; masked values meet a zero probability in the product, so the
@@ -72,12 +72,22 @@ __device__ __forceinline__ int unit_tiles(int len, int cap) {
   return len < 0 || len > cap ? 0 : (len + kBN - 1) / kBN + 1;
 }
 
-// the first tile of worker w's share
+// What a unit counts in the shares: its tiles and, before them, the time that its beginning and end cost, in tiles: loads that
+// wait behind the tiles' copies (gate, tree, the next Q), the epilogue, the first products.  Without it the workers that get many
+// short units end last (64 ragged sequences x 16 nodes: 280 us at a cost of 0 tiles, 264 at 2, 249 at 4, 236 at 6, 226 at 8 and 10, 227 at
+// 16; x 64 nodes 623 at 0, 500 at 8; one sequence of 32,768 keys x 21 nodes 59 and 53; equal lengths and heads of 128: 2% or less from 6 on).
+constexpr int kUnitCost = 8;
+__device__ __forceinline__ int unit_weight(int len, int cap) {
+  const int nt = unit_tiles(len, cap);
+  return nt > 0 ? nt + kUnitCost : 0;
+}
+
+// the first position of worker w's share
 __device__ __forceinline__ long long share_begin(long long total, int w, int workers) {
   return total / workers * w + min(total % workers, static_cast<long long>(w));
 }
 
-// the worker that takes tile x
+// the worker that takes position x
 __device__ __forceinline__ int share_owner(long long total, long long x, int workers) {
   const long long q = total / workers, r = total % workers;
   return static_cast<int>(x < r * (q + 1) ? x / (q + 1) : r + (x - r * (q + 1)) / q);
@@ -92,7 +102,7 @@ __device__ long long locate(const int* cache_len, int N, int cap, int H_kv, int 
   const int per = (N + n_thr - 1) / n_thr;
   const int n0 = min(N, tid * per), n1 = min(N, n0 + per);
   long long sum = 0;
-  for (int n = n0; n < n1; ++n) sum += unit_tiles(cache_len[n], cap);
+  for (int n = n0; n < n1; ++n) sum += unit_weight(cache_len[n], cap);
   chunk_s[tid] = sum * H_kv;
   if (tid == 0) {
     *seq_s = N;
@@ -122,7 +132,7 @@ __device__ long long locate(const int* cache_len, int N, int cap, int H_kv, int 
   const long long x = share_begin(total, w, workers);
   long long at = chunk_s[tid];
   for (int n = n0; n < n1; ++n) {
-    const long long next = at + static_cast<long long>(unit_tiles(cache_len[n], cap)) * H_kv;
+    const long long next = at + static_cast<long long>(unit_weight(cache_len[n], cap)) * H_kv;
     if (at <= x && x < next) {
       *seq_s = n;
       *base_s = at;
@@ -204,21 +214,22 @@ struct Walk {
   long long base, x, end;
   __device__ __forceinline__ bool next(Segment& s) {
     while (x < end && seq < N) {
-      const int len = cache_len[seq], nt = unit_tiles(len, cap);
+      const int len = cache_len[seq], w = unit_weight(len, cap);
       const long long off = x - base;
-      if (off >= static_cast<long long>(nt) * H_kv) {
-        base += static_cast<long long>(nt) * H_kv;
+      if (off >= static_cast<long long>(w) * H_kv) {
+        base += static_cast<long long>(w) * H_kv;
         ++seq;
         continue;
       }
       s.n = seq;
       s.len = len;
-      s.nt = nt;
-      s.kvh = static_cast<int>(off / nt);
-      s.t0 = static_cast<int>(off % nt);
-      s.nj = static_cast<int>(min(static_cast<long long>(nt - s.t0), end - x));
-      x += s.nj;
-      return true;
+      s.nt = w - kUnitCost;
+      s.kvh = static_cast<int>(off / w);
+      const int at = static_cast<int>(off % w), n = static_cast<int>(min(static_cast<long long>(w - at), end - x));
+      s.t0 = max(at - kUnitCost, 0);
+      s.nj = max(at + n - kUnitCost, 0) - s.t0;
+      x += n;
+      if (s.nj > 0) return true;  // (else the share ends before the unit's first tile)
     }
     return false;
   }
