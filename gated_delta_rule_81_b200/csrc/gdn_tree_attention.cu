@@ -548,6 +548,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                   for (int e = 0; e < 32; ++e) o[e] *= f;
                   tmem_st32(trow + C::kColO + (D / 2) * hc + 32u * c, o);
                 }
+                tmem_wait_st();  // (the tree's tile has no P of the second half to wait for)
                 l *= f;
               }
             }
@@ -574,7 +575,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           }
         }
         if (in_tree || lim < kBN) {
-          // values that some row may not see: zero them in place before the product reads the tile
+          // values that some row may not see: zero them in place before the product reads the tile.  A slot's wait tells its last
+          // fill from the one two before by parity only, and the slot of V_j's second half held V_{j-1}'s first (ring of 5): that
+          // must have been read, or the wait could end on the fill before and the wrong tile be zeroed.
+          if (j >= 1) ok = ok && mbar_wait_warp(&sh.pv_done[(tl - 1) & 1], ((tl - 1) >> 1) & 1, ab);
           const uint32_t ld = rb + ring_v(j, sg.nj);
           for (int i = 0; i < (in_tree ? 1 : 2); ++i) {
             const uint32_t st = (ld + i) % kSlots;

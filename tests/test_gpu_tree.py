@@ -296,6 +296,27 @@ def test_attention_tree_two_streams_and_rows_beside_the_output():
         assert torch.equal(b[1:-1], w) and bool((b[0] == 5).all()) and bool((b[-1] == 5).all())
 
 
+@pytest.mark.parametrize("D,H,Hkv", [(256, 24, 4), (128, 32, 8)])
+def test_attention_tree_repeats_bitwise_under_load(D, H, Hkv):
+    """Many ragged contexts whose tiles stream from memory as fast as it gives them: every repetition gives the same bits,
+    whatever the order in which copies land."""
+    N, T, cap = 64, 16, 4096
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)
+    kc, vc = rnd(N, cap, Hkv, D), rnd(N, cap, Hkv, D)
+    q, kt, vt, gate = rnd(N * T, H * D), rnd(N * T, Hkv * D), rnd(N * T, Hkv * D), rnd(N * T, H * D)
+    lens = torch.tensor([300 + (cap - 300) * ((i * 7) % N) // (N - 1) for i in range(N)], dtype=torch.int32, device="cuda")
+    parent = dev_tree(make_tree("holes", N, T, 3))
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    want = None
+    for rep in range(60):
+        flush.fill_(rep)
+        out = gdn.attention_tree(q.view(N * T, H, D), kt.view(N * T, Hkv, D), vt.view(N * T, Hkv, D), kc, vc, lens, parent,
+                                 g=gate.view(N * T, H, D))
+        want = out if want is None else want
+        assert torch.equal(out, want), rep
+
+
 def test_tree_bad_parents_are_absent_and_reported():
     c = attn_case(1, 5, 8, 2, 128, [40], "chain", seed=7)
     want = attn_run(c).view(5, -1)
