@@ -480,6 +480,29 @@ def test_decode_tree_large_batch_with_bad_slots_and_nodes(T, H_v):
         assert torch.equal(alone.view(T, H_v, 128).view(torch.int16), out[n].view(torch.int16)), n
 
 
+@pytest.mark.parametrize("T,N", [(5, 90), (13, 2), (30, 2), (40, 2), (64, 90)])
+def test_decode_tree_pools_and_rows_aligned_to_16_bytes_only(T, N):
+    """A state pool, conv pool and rows that begin 16 bytes into their buffers: the results of aligned ones, bitwise."""
+    H_k, H_v = 2, 6
+    c = delta_case(N, T, H_k, H_v, "holes", seed=T)
+    want = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"])
+
+    def moved(x):
+        step = 16 // x.element_size()
+        buf = torch.zeros(x.numel() + 2 * step, dtype=x.dtype, device="cuda")
+        y = buf[step:step + x.numel()].view(x.shape)
+        y.copy_(x)
+        assert y.data_ptr() % 32 == 16
+        return y
+
+    d = c["dev"]
+    m = {k: moved(d[k]) for k in ("q", "k", "v", "z", "conv_w")}  # (kept: the descriptor holds addresses)
+    s = gdn.make_inputs(m["q"], m["k"], m["v"], d["a"], d["b"], m["z"], m["conv_w"], d["A_log"], d["norm_w"], scale=c["inp"]["scale"])
+    state, conv, out = moved(c["d_state"]), moved(c["d_conv"]), moved(torch.zeros_like(want))
+    gdn.decode_tree(s, N, T, c["parent"], state, conv, state_slot=c["d_slot"], out=out)
+    assert torch.equal(out, want)
+
+
 def test_decode_tree_and_commit_past_32_bit_offsets():
     """A pool of more than 2^31 state elements: the sequence's slot is the last."""
     T, H_k, H_v, slots = 9, 16, 48, 2800
