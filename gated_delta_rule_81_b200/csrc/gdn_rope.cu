@@ -29,16 +29,24 @@ __device__ __forceinline__ void unpack8(uint4 u, float2 (&f)[4]) {
 // 8l .. 8l + 7 (one 16-byte load each).  Cosines, sines and norm weights stay in registers over the heads, so that a head
 // costs little more than its own arithmetic in packed fp32: with them fetched per head, and q, k and v told apart per
 // load, the kernel spent 180 instructions per 8 elements and was bound by issuing them (179 us for 32,768 tokens of 48 heads of
-// 128; the bytes take 123 us); now 154 us, 5.2 TB/s, at 39% of the issue slots.  Few tokens are split into many items of few heads.
+// 128; the bytes take 123 us); now 151 us, 5.3 TB/s, at 39% of the issue slots.  Few tokens are split into
+// many items of few heads: items below `whole` are whole tokens, the others `per` heads of one, `splits` to a token.
 template <int W, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 4)
-    qk_norm_rope_kernel(const __grid_constant__ gdn_rope rope, const __grid_constant__ RopeParams p, int splits, int per) {
+    qk_norm_rope_kernel(const __grid_constant__ gdn_rope rope, const __grid_constant__ RopeParams p, long long whole, int splits, int per) {
   constexpr int kGroups = kRopeThreads / W;
   __shared__ int tree_s[kGroups][kMaxNodes];
+  // frequencies: from parameter memory lanes read one after the other, which a long call is spared (154 -> 151 us for 32,768 tokens)
+  // and a short one would pay the barrier for (4.2 -> 4.5 us for 21)
+  __shared__ unsigned long long turns_s[GDN_ROPE_MAX_HEAD_DIM / 2];
+  if (whole > 0) {
+    for (int i = threadIdx.x; i < rope.rotary_dim / 2; i += kRopeThreads) turns_s[i] = rope.turns[i];
+    __syncthreads();
+  }
   const int grp = threadIdx.x / W, l = threadIdx.x % W;
   const unsigned mask = W == 32 ? 0xffffffffu : ((1u << (W & 31)) - 1u) << ((threadIdx.x & 31) / W * W);
   const long long item = static_cast<long long>(blockIdx.x) * kGroups + grp;
-  const long long t = item / splits;
+  const long long t = item < whole ? item : whole + (item - whole) / splits;
   if (t >= p.n_tok) return;  // whole groups
   const int D = rope.head_dim, R = rope.rotary_dim;
   const bool on = 8 * l < D, turned = 8 * l < R;
@@ -70,7 +78,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     float c[4], s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const unsigned long long turn = static_cast<unsigned long long>(pos) * rope.turns[f0 + i];
+      const unsigned long long turn = static_cast<unsigned long long>(pos) * (whole > 0 ? turns_s[f0 + i] : rope.turns[f0 + i]);
       sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: in half turns
       c[i] *= rope.amplitude;
       s[i] *= rope.amplitude;
@@ -150,8 +158,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     }
   };
   // this item's heads among q | k | v
-  const int b = static_cast<int>(item % splits) * per, e = b + per;
   const int k0 = p.H_q, v0 = p.H_q + p.H_kv, end = v0 + (p.v ? p.H_kv : 0);
+  const int b = item < whole ? 0 : static_cast<int>((item - whole) % splits) * per, e = item < whole ? end : b + per;
   if (b < k0) heads(p.q + t * p.ld_q, p.q_out + t * p.ld_qo, p.q_norm_w, b, min(e, k0));
   if (row < 0) return;
   if (b < v0 && e > k0) heads(p.k + t * p.ld_k, p.k_out + row * p.ld_ko, p.k_norm_w, max(b, k0) - k0, min(e, v0) - k0);
@@ -168,17 +176,24 @@ template <int W>
 void rope_launch(const gdn_rope& rope, const RopeParams& p, cudaStream_t stream) {
   constexpr int kGroups = kRopeThreads / W;
   const int H = p.H_q + p.H_kv + (p.v ? p.H_kv : 0);
-  // heads per item: few enough that the items fill the GPU, in rounds of kRopeFlight, and all of a token's at most
+  // Tokens whole while they fill the GPU round by round; left over ones that fill no more than a third of a round are split into
+  // items of so few heads, in rounds of kRopeFlight, that they take one short round.  An item forms its token's factors again, which
+  // more of them would not gain back (20,000 tokens of 48 heads, 2.11 rounds: 94 us split, 105 whole; 16,384, 1.73 rounds: 95 and 78;
+  // 32,768, 3.46 rounds: 152 and 151, and 190 with all tokens in halves).
   const long long want = 148LL * 4 * kGroups;  // groups resident at once
-  long long per = (p.n_tok * H + want - 1) / want;
+  long long whole = p.n_tok / want * want;
+  if ((p.n_tok - whole) * 3 > want && whole > 0) whole = p.n_tok;
+  const long long rest = p.n_tok - whole;
+  long long per = (rest * H + want - 1) / want;
   per = (per + kRopeFlight - 1) / kRopeFlight * kRopeFlight;
   if (per > H) per = H;
+  if (per < 1) per = 1;
   const int splits = static_cast<int>((H + per - 1) / per);
-  const unsigned grid = static_cast<unsigned>((p.n_tok * splits + kGroups - 1) / kGroups);
+  const unsigned grid = static_cast<unsigned>((whole + rest * splits + kGroups - 1) / kGroups);
   if (rope.layout == GDN_ROPE_INTERLEAVED)
-    qk_norm_rope_kernel<W, true><<<grid, kRopeThreads, 0, stream>>>(rope, p, splits, static_cast<int>(per));
+    qk_norm_rope_kernel<W, true><<<grid, kRopeThreads, 0, stream>>>(rope, p, whole, splits, static_cast<int>(per));
   else
-    qk_norm_rope_kernel<W, false><<<grid, kRopeThreads, 0, stream>>>(rope, p, splits, static_cast<int>(per));
+    qk_norm_rope_kernel<W, false><<<grid, kRopeThreads, 0, stream>>>(rope, p, whole, splits, static_cast<int>(per));
 }
 
 }  // namespace

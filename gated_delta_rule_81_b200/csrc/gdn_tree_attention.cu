@@ -7,9 +7,9 @@
 //
 // Work split.  A unit is one (sequence, KV head): its tiles are ceil(cache_len / 128) tiles of the cache and
 // one tile of the tree (64 keys).  The tiles of all units in a row, each unit's preceded by what its beginning and
-// end cost (kUnitCost), are cut into W equal shares, one per worker, so that ragged lengths balance and a single long sequence still fills the GPU; a unit cut between
-// workers leaves partial (o, m, l) that a second kernel joins.  Rows beyond 128 go to further CTAs (blockIdx.x)
-// of the same worker, which read the same tiles at about the same time, from L2.
+// end cost (kUnitCost), are cut into W equal shares, one per worker, so that ragged lengths balance and a single long
+// sequence still fills the GPU; a unit cut between workers leaves partial (o, m, l) that a second kernel joins.  Rows beyond
+// 128 go to further CTAs (blockIdx.x) of the same worker, which read the same tiles at about the same time, from L2.
 //
 // A CTA: warps 0-7 softmax and epilogue (thread = query row = TMEM lane; warps w and w + 4 share a row's
 // 128 scores and O's D columns in halves), warp 8 TMA, warp 9 tcgen05.mma.  TMEM: O (D columns) | S in two buffers of
@@ -610,7 +610,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       // ---- every S of this segment has been read: the next one's Q may take its place, and its first S run beside
       // the epilogue
       if (sg.t0 == 0 && !tree_end)  // the unit goes on in later shares
-        if (threadIdx.x == 0 && mt == 0) p.cut[worker] = make_int4(sg.n, sg.kvh, first ? 0 : 1, share_owner(sh.total, walk.x - 1 + (sg.nt - sg.nj), p.workers));
+        if (threadIdx.x == 0 && mt == 0)
+          p.cut[worker] = make_int4(sg.n, sg.kvh, first ? 0 : 1, share_owner(sh.total, walk.x - 1 + (sg.nt - sg.nj), p.workers));
       Segment nx;
       have = walk.next(nx);
       if (have) fetch_q(nx);

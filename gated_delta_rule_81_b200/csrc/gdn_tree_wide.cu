@@ -95,7 +95,8 @@ __device__ __forceinline__ int image_at(int t, int j) {
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 152;"); }
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
 
-// kAligned32: the state begins at a multiple of 32 bytes, so that a lane's 32 can be loaded at once (255 us for 64 sequences x 61 nodes, else 272)
+// kAligned32: the state begins at a multiple of 32 bytes, so that a lane's 32 can be loaded at once (64 sequences x 61 nodes 255 us,
+// else 272)
 template <bool kAligned32>
 __global__ void __launch_bounds__(kThreads, 1) decode_tree_wide_kernel(const __grid_constant__ TreeParams p) {
   extern __shared__ uint8_t tw_smem[];

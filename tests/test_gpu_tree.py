@@ -106,6 +106,27 @@ def test_qk_norm_rope(D, R, inter, scaling, H_q, H_kv, n, norm):
     assert bool((k_out[rest.cuda()] == 7).all()) and bool((v_out[rest.cuda()] == 7).all())
 
 
+@pytest.mark.parametrize("D,H_q,H_kv,n", [(256, 3, 1, 4736 + 37), (128, 5, 2, 2 * 9472 + 900), (128, 2, 1, 9472), (64, 3, 2, 18944 + 9000)])
+def test_qk_norm_rope_more_tokens_than_fit_at_once(D, H_q, H_kv, n):
+    """Rounds of whole tokens, then the tokens left over, split or whole: bitwise the results of small calls."""
+    g = torch.Generator().manual_seed(n)
+    proj = torch.randn(n, (H_q + 2 * H_kv) * D, generator=g).to(torch.bfloat16).cuda()
+    q, k, v = (x.unflatten(1, (-1, D)) for x in (proj[:, :H_q * D], proj[:, H_q * D:(H_q + H_kv) * D], proj[:, (H_q + H_kv) * D:]))
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(torch.bfloat16).cuda()
+    pos = torch.randint(0, 300000, (n,), generator=g, dtype=torch.int32).cuda()
+    rows = torch.randperm(n, generator=g).cuda()
+    rope = gdn.make_rope(D, D // 2, base=1e6)
+    outs = []
+    for step in (n, 611):
+        k_out, v_out = (torch.zeros(n, H_kv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        y = torch.cat([gdn.qk_norm_rope(rope, q[i:i + step], k[i:i + step], v[i:i + step], q_norm_w=w, k_norm_w=w,
+                                        positions=pos[i:i + step], rows=rows[i:i + step], k_out=k_out, v_out=v_out)[0]
+                       for i in range(0, n, step)])
+        outs.append((y, k_out, v_out))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert torch.equal(outs[0][2][rows], v)
+
+
 def test_qk_norm_rope_in_place_parts_and_bad_rows():
     D, n = 128, 37
     g = torch.Generator().manual_seed(5)
