@@ -62,7 +62,7 @@ struct TaParams {
   int G, m_tiles, workers, slot_rows;
   float scale_log2e;
   float4* part_o;   // [workers][2][m_tiles][D / 4][slot_rows]: rows side by side, as the lanes that write and read them
-  float2* part_ml;  // [workers][2][m_tiles][slot_rows]: maximum (log2 units) and sum; an absent node's: -inf, 0
+  float2* part_ml;  // [workers][2][m_tiles][slot_rows]: maximum (log2 units) and sum; an absent node's: -inf, -1 (no sum is negative)
   int4* cut;        // [workers]: the unit that begins in a worker's share and ends in a later one's: sequence
                     // (-1: none), KV head, which of the worker's partials, the last worker
 };
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         const unsigned long long bad = sh.bad_v & mask;
         const int slot = (worker * 2 + (first ? 0 : 1)) * p.m_tiles + mt;
         const float inv_l = 1.0f / l_row;
-        if (!whole && valid && hc == 0) p.part_ml[slot * p.slot_rows + r] = live ? make_float2(m, l_row) : make_float2(-INFINITY, 0.f);
+        if (!whole && valid && hc == 0) p.part_ml[slot * p.slot_rows + r] = live ? make_float2(m, l_row) : make_float2(-INFINITY, -1.f);
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           float o[32];
@@ -711,6 +711,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_tree_join_kernel(const
   if (a.g) gate = reinterpret_cast<const uint2*>(a.g + tok * a.ld_g + static_cast<long long>(h) * D)[c4];
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -INFINITY, L = 0.f;
+  bool live = true;
   for (int wb = w0; wb <= w1; wb += kFlight) {
     float2 ml[kFlight];
     float4 v[kFlight];
@@ -721,24 +722,27 @@ __global__ void __launch_bounds__(kJoinThreads) attention_tree_join_kernel(const
       ml[i] = p.part_ml[slot * p.slot_rows + r];
       v[i] = p.part_o[(static_cast<long long>(slot) * (D / 4) + c4) * p.slot_rows + r];
     }
+    live = !(ml[0].y < 0.f);
+    if (!live) break;  // an absent node's row: its values were never written
     float top = M;
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) top = fmaxf(top, ml[i].x);
-    if (top == -INFINITY) continue;  // an absent node's row: its partials were never written
-    const float f0 = ex2(M - top);
+    // A piece whose scores are all NaN (or -inf) has no maximum either: its sum is NaN (or 0), and is taken like any other.
+    const float at = top == -INFINITY ? 0.f : top;
+    const float f0 = ex2(M - at);
     M = top;
     L *= f0;
     y = make_float4(y.x * f0, y.y * f0, y.z * f0, y.w * f0);
 #pragma unroll
     for (int i = 0; i < kFlight; ++i) {
       if (wb + i > w1) break;
-      const float f = ex2(ml[i].x - M);
+      const float f = ex2(ml[i].x - at);
       L = fmaf(ml[i].y, f, L);
       y = make_float4(fmaf(v[i].x, f, y.x), fmaf(v[i].y, f, y.y), fmaf(v[i].z, f, y.z), fmaf(v[i].w, f, y.w));
     }
   }
   uint2 out = make_uint2(0u, 0u);
-  if (M > -INFINITY) {
+  if (live) {
     const float inv = 1.0f / L;
     float o[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
     if (a.g) {

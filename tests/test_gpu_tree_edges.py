@@ -1,0 +1,72 @@
+"""Tree calls at the edges of what they take: rows whose result has to be NaN."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_gpu_tree import attn_case, attn_run
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ gdn_attention_tree
+
+# one sequence cut between many workers, a few sequences, a batch whose units are cut here and whole there
+SPLITS = [(1, 3, 24, 4, 256, [3000]), (2, 5, 8, 2, 128, [700, 2100]), (300, 2, 2, 1, 128, [(i * 37) % 300 for i in range(300)])]
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("N,T,H,Hkv,D,lens", SPLITS)
+def test_attention_tree_query_that_is_not_finite_gives_nan(N, T, H, Hkv, D, lens, value):
+    """A node's query head with an element that is not finite has scores that no softmax can weigh: NaN by the definition,
+    however the work is split, and no other row changes."""
+    c = attn_case(N, T, H, Hkv, D, lens, "chain", seed=51)
+    clean = attn_run(c).view(N, T, H, D)
+    c["q"].view(N, T, H, D)[:, T - 1, H - 1, 7] = value
+    out = attn_run(c).view(N, T, H, D)
+    assert bool(torch.isnan(out[:, T - 1, H - 1]).all())
+    rest = torch.ones(N, T, H, dtype=torch.bool, device="cuda")
+    rest[:, T - 1, H - 1] = False
+    assert torch.equal(out[rest], clean[rest])
+
+
+@pytest.mark.parametrize("N,T,H,Hkv,D,lens", SPLITS)
+def test_attention_tree_row_whose_scores_are_all_minus_infinity_gives_nan(N, T, H, Hkv, D, lens):
+    """Every visible score -inf: 0 / 0 by the definition; an absent node's row stays zeros beside it."""
+    c = attn_case(N, T, H, Hkv, D, lens, "chain", seed=52)
+    c["parent"][:, T - 1] = -2
+    c["q"].view(N, T, H, D)[:, 0, 0, 3] = -float("inf")
+    c["kc"][..., 3] = c["kc"][..., 3].abs() + 0.125
+    c["kt"][..., 3] = c["kt"][..., 3].abs() + 0.125
+    out = attn_run(c).view(N, T, H, D)
+    assert bool(torch.isnan(out[:, 0, 0]).all()) and bool((out[:, T - 1] == 0).all())
+    assert bool(torch.isfinite(out[:, :T - 1, 1:]).all())
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(1, 1, 128), (24, 4, 256)])
+def test_attention_tree_nan_keys_at_the_cache_s_beginning_give_nan(H, Hkv, D):
+    """Keys that are NaN in a long cache's first 16 tiles of 128: every node sees them, whichever workers'
+    partials they fall into."""
+    c = attn_case(1, 2, H, Hkv, D, [6000], "chain", seed=53)
+    c["kc"][0, :16 * 128] = float("nan")
+    assert bool(torch.isnan(attn_run(c)).all())
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens", [[150], [40] * 200])
+def test_attention_tree_key_that_is_not_finite_reaches_its_descendants(value, lens):
+    """A node whose key and value are NaN or infinite: NaN for every row that sees it (infinite scores of both signs, or an
+    infinite value under a weight of NaN), nothing for the others."""
+    N, T, bad, H, D = len(lens), 24, 3, 24, 256
+    c = attn_case(N, T, H, 4, D, lens, "holes", seed=9)
+    clean = attn_run(c).view(N, T, H, D)
+    for x in (c["kt"], c["vt"]):
+        x[bad] = value
+    out = attn_run(c).view(N, T, H, D)
+    hit = torch.zeros(N, T, dtype=torch.bool, device="cuda")
+    hit[0] = torch.tensor([bad in p for p in oracle.tree.paths(c["rows"][0])], device="cuda")
+    assert bool(hit.any()) and torch.equal(out[~hit], clean[~hit])
+    ref = oracle.tree.attention_tree(c["q"][:T].cpu(), c["kt"][:T].cpu(), c["vt"][:T].cpu(), c["kc"][:1].cpu(), c["vc"][:1].cpu(),
+                                     lens[:1], c["rows"][:1], c["g"][:T].cpu())["out"]
+    want = torch.from_numpy(np.isnan(ref)).cuda()
+    assert torch.equal(torch.isnan(out[0])[hit[0]], want[hit[0]])
