@@ -225,12 +225,13 @@ extern "C" gdn_status gdn_rope_init(gdn_rope* rope, int head_dim, int rotary_dim
   if (scaling == GDN_ROPE_NTK && rotary_dim > 0) b *= powl(factor, static_cast<long double>(rotary_dim) / (rotary_dim - 2));
   double lo = 0, hi = 0;
   if (scaling == GDN_ROPE_YARN && half > 0) {
-    // the (fractional) pair that turns `beta` times within original_len positions
+    // the (fractional) pair that turns `beta` times within original_len positions; the one of beta_slow may lie beyond the last
+    // pair, half - 1, and the ramp then does not reach 1
     auto pair = [&](double beta) {
       return rotary_dim * std::log(original_len / (beta * static_cast<double>(kTwoPi))) / (2.0 * std::log(base));
     };
     lo = std::fmax(std::floor(pair(beta_fast)), 0.0);
-    hi = std::fmin(std::ceil(pair(beta_slow)), half - 1.0);
+    hi = std::fmin(std::ceil(pair(beta_slow)), rotary_dim - 1.0);
   }
   *rope = gdn_rope{};
   rope->head_dim = head_dim;

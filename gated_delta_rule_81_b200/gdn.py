@@ -587,7 +587,8 @@ def make_rope(head_dim: int, rotary_dim: int | None = None, *, base: float = 1e7
               scaling: str = "none", factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0,
               beta_slow: float = 1.0, eps: float = 1e-6) -> GdnRope:
     """gdn_rope_init: the table of a rotary embedding on the first rotary_dim dims of each head (default all),
-    scaling "none", "linear", "ntk" or "yarn"; eps is the norms'.  Made once and kept."""
+    scaling "none", "linear", "ntk" or "yarn"; eps is the norms'.  Made once and kept; `amplitude`, the factor on
+    cosine and sine, may be set on the result."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, not {scaling!r}")
     rope = GdnRope()

@@ -455,9 +455,12 @@ gdn_status gdn_layer_tree_commit(const gdn_layer* L, int N, int T, const int* pa
  *            GDN_ROPE_LINEAR  theta_i / factor (positions interpolated)
  *            GDN_ROPE_NTK     base * factor^(r / (r - 2)) in place of base, r = rotary_dim
  *            GDN_ROPE_YARN    theta_i (1 - ramp_i) + theta_i / factor * ramp_i with ramp_i rising from 0 to 1
- *                             between the pairs that turn beta_fast and beta_slow times within
- *                             original_len positions, and cosine and sine times 0.1 ln(factor) + 1
- * gdn_rope_init fills the table once; the struct is then only read.  turns[i] is theta_i / 2 pi in units of
+ *                             between the pairs that turn beta_fast and beta_slow times within original_len
+ *                             positions: ramp_i = min(max((i - low) / (high - low), 0), 1), low = max(floor(c(beta_fast)), 0),
+ *                             high = min(ceil(c(beta_slow)), r - 1), c(b) = r ln(original_len / 2 pi b) / (2 ln base);
+ *                             and cosine and sine times `amplitude`, 0.1 ln(factor) + 1
+ * gdn_rope_init fills the table once; the struct is then only read.  (A checkpoint that scales cosine and sine by a
+ * factor of its own: store that in `amplitude` after gdn_rope_init.)  turns[i] is theta_i / 2 pi in units of
  * 2^-64 turns, so that position * turns[i] modulo 2^64 is the angle whatever the position: no angle of a
  * far position loses bits before its reduction.  Positions may be any int32.
  * head_dim: a multiple of 8, 8 .. GDN_ROPE_MAX_HEAD_DIM; rotary_dim: a multiple of 16, 0 .. head_dim (0: no

@@ -106,7 +106,7 @@ def rope_frequencies(rotary_dim, base, scaling="none", factor=1.0, original_len=
     if scaling == "yarn":
         def pair(beta):
             return r * math.log(original_len / (beta * 2 * math.pi)) / (2 * math.log(base))
-        low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), half - 1)
+        low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), r - 1)
         ramp = np.clip((np.arange(half) - low) / max(high - low, 1e-3), 0, 1)
         return theta * (1 - ramp) + theta / factor * ramp, 0.1 * math.log(factor) + 1.0
     return theta, 1.0

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import oracle
+from gated_delta_rule_81_b200 import gdn
 from test_gpu_tree import attn_case, attn_run
 
 pytestmark = pytest.mark.gpu
@@ -70,3 +71,16 @@ def test_attention_tree_key_that_is_not_finite_reaches_its_descendants(value, le
                                      lens[:1], c["rows"][:1], c["g"][:T].cpu())["out"]
     want = torch.from_numpy(np.isnan(ref)).cuda()
     assert torch.equal(torch.isnan(out[0])[hit[0]], want[hit[0]])
+
+
+# ------------------------------------------------------------------ gdn_qk_norm_rope
+
+def test_rope_amplitude_of_the_caller():
+    """A factor on cosine and sine that the caller stores in the table."""
+    q = torch.randn(9, 3, 128, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(9, dtype=torch.int32, device="cuda") * 977
+    rope = gdn.make_rope(128, 64, scaling="yarn", factor=1.0, original_len=4096)
+    want = gdn.qk_norm_rope(rope, q, positions=pos)[0]
+    rope.amplitude = 2.0
+    got = gdn.qk_norm_rope(rope, q, positions=pos)[0]
+    assert torch.equal(got[..., :64], 2 * want[..., :64]) and torch.equal(got[..., 64:], want[..., 64:])

@@ -184,6 +184,24 @@ def test_rope_table(lib, scaling, R):
     assert all(rope.turns[i] == 0 for i in range(R // 2, 128))
 
 
+def test_yarn_ramp_past_the_last_pair(lib):
+    """The pair that turns once lies beyond the last one: the ramp ends there, not at the last pair.  Numbers written out."""
+    # 8 pairs, base 10^4: 16 ln(32768 / 2 pi 32) / 2 ln 10^4 = 4.42, 16 ln(32768 / 2 pi) / 2 ln 10^4 = 7.43: from 4 to 8
+    kw = dict(base=1e4, scaling="yarn", factor=8.0, original_len=32768)
+    want = [1, 10 ** -0.5, 10 ** -1, 10 ** -1.5, 10 ** -2,
+            10 ** -2.5 * (0.75 + 0.25 / 8), 10 ** -3 * (0.5 + 0.5 / 8), 10 ** -3.5 * (0.25 + 0.75 / 8)]
+    rope = gdn.make_rope(64, 16, **kw)
+    np.testing.assert_allclose([rope.turns[i] / 2.0 ** 64 * 2 * math.pi for i in range(8)], want, rtol=1e-13)
+    np.testing.assert_allclose(oracle.tree.rope_frequencies(16, **kw)[0], want, rtol=1e-13)
+    # 64 pairs at 131,072 positions: 45.03 and 69.11, so from 45 to 70; the last pair, 63, at 18 / 25
+    kw = dict(base=1e4, scaling="yarn", factor=16.0, original_len=131072)
+    rope = gdn.make_rope(128, **kw)
+    for i, ramp in ((45, 0.0), (50, 0.2), (55, 0.4), (63, 0.72)):
+        want = 10 ** (-4 * i / 64) * (1 - ramp + ramp / 16)
+        assert rope.turns[i] / 2.0 ** 64 * 2 * math.pi == pytest.approx(want, rel=1e-13)
+        assert oracle.tree.rope_frequencies(128, **kw)[0][i] == pytest.approx(want, rel=1e-13)
+
+
 def test_layer_tree_sizes_and_refusals(lib):
     assert lib.gdn_layer_tree_workspace_size(16, 48, 2, 65) == 0
     assert lib.gdn_layer_tree_workspace_size(16, 48, 1, 64) >= 64 * (16480 + 6144) * 2
