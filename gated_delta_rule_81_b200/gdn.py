@@ -565,7 +565,8 @@ def decode_tree(inp: GdnInputs, N: int, T: int, parent, state, conv_state, state
 def decode_tree_commit(inp: GdnInputs, N: int, T: int, parent, accepted, state, conv_state, state_slot=None, *,
                        state_out=None, conv_out=None, err=None):
     """gdn_decode_tree_commit: state and conv_state advanced along each sequence's path to node accepted[n]
-    (device int32 [N], -1: none), in place unless state_out / conv_out are given.  Returns both."""
+    (device int32 [N], -1: none), in place unless state_out / conv_out are given.  `inp`'s q, k, v, a and b hold what
+    they held at decode_tree (the last raw rows become the conv state).  Returns both."""
     slots, dev = _want_pool(inp.H_k, inp.H_v, state, conv_state)
     if state_out is None:
         state_out = state

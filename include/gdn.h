@@ -419,8 +419,9 @@ gdn_status gdn_decode_tree(const gdn_inputs* in, int N, int T, const int* parent
 /*
  * The commit of gdn_decode_tree: applies the tokens of the accepted path, in order, exactly as
  * gdn_decode_step calls would (same arithmetic: the states are bitwise those of decoding the
- * path token by token).  in, N, T, parent: as in the gdn_decode_tree call (q and z are not read,
- * but have to be valid).
+ * path token by token).  in, N, T, parent: as in the gdn_decode_tree call, with the contents that q, k, v, a
+ * and b had there: the path's last raw rows of q, k and v become the conv state.  (z is not read, but has to
+ * be a valid argument.)
  *   state_in, conv_in    the pools as in gdn_decode_tree, read
  *   state_out, conv_out  the pools written, the same slots; each either exactly its input (in place) or
  *                        without overlap.  Slots no sequence uses stay as they were.

@@ -5,7 +5,7 @@ import torch
 
 import oracle
 from gated_delta_rule_81_b200 import gdn
-from test_gpu_tree import attn_case, attn_run
+from test_gpu_tree import attn_case, attn_run, delta_case
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,16 @@ def test_rope_amplitude_of_the_caller():
     rope.amplitude = 2.0
     got = gdn.qk_norm_rope(rope, q, positions=pos)[0]
     assert torch.equal(got[..., :64], 2 * want[..., :64]) and torch.equal(got[..., 64:], want[..., 64:])
+
+
+# ------------------------------------------------------------------ gdn_decode_tree_commit
+
+def test_decode_tree_commit_reads_the_path_s_query_rows():
+    """The q channels of the conv state are the path's last three raw q rows: what q holds at the commit counts."""
+    T, H_k, H_v = 6, 2, 6
+    c = delta_case(1, T, H_k, H_v, "chain", seed=71)
+    acc = torch.tensor([T - 1], dtype=torch.int32, device="cuda")
+    C = c["d_conv"].clone()
+    gdn.decode_tree_commit(c["s"], 1, T, c["parent"], acc, c["d_state"].clone(), C, state_slot=c["d_slot"])
+    q = c["dev"]["q"].reshape(T, H_k * 128)
+    assert torch.equal(C[int(c["slot"][0]), :, :H_k * 128], q[T - 3:])

@@ -2,6 +2,7 @@
 launch.  Addresses are made up; no call here reaches a launch."""
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -74,6 +75,15 @@ def test_decode_tree_commit_refusals(lib):
     assert commit(lib, s_out=ACC) == ALIAS
     assert commit(lib, s_out=fake_inputs().q) == ALIAS
     assert commit(lib, c_in=CONV + 8, c_out=CONV + 8) == MISALIGNED
+
+
+def test_header_says_what_the_commit_reads():
+    """Every raw row of the path becomes conv state, q's too: the contract may not let a caller reuse q before the commit."""
+    with open(os.path.join(build.INCLUDE, "gdn.h")) as f:
+        text = " ".join(f.read().replace("*", " ").split())
+    doc = text[text.index("The commit of gdn_decode_tree:"):text.index("gdn_status gdn_decode_tree_commit(")]
+    assert "q and z are not read" not in doc
+    assert "last raw rows of q, k and v become the conv state" in doc
 
 
 def attention(lib, H=24, Hkv=4, D=256, scale=0.0625, N=2, T=4, cap=100, ld_q=None, ld_kt=None, out=OUT, ws=7 << 36, nb=None,
