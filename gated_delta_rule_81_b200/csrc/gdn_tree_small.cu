@@ -308,7 +308,12 @@ __global__ void __launch_bounds__(kWorkers, 4) decode_tree_small_kernel(const __
     v0[kVRow + 8] = x_q[3];
   }
 
-  // ---- gated RMS norm, a warp per (node, head), a few at a time
+  // ---- gated RMS norm, a warp per (node, head), a few at a time.  Every warp's rows of o are awaited; a warp without a pair
+  // only announces its own.
+  if (warp >= T * HP) {
+    bar_arrive(1, kWorkers);
+    return;
+  }
   float nw[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) nw[e] = __bfloat162float(p.norm_w[4 * lane + e]);  // norm_w: aligned to 2 bytes only
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(kWorkers, 4) decode_tree_small_kernel(const __
       const int x = min(x0 + 8 * i, T * HP - 1);
       zz[i] = *reinterpret_cast<const uint2*>(p.z + (tok0 + x / HP) * p.sz + static_cast<long long>(hv0 + x % HP) * kD + 4 * lane);
     }
-    if (x0 == warp) __syncthreads();  // every warp's rows of o (the first round's loads are on their way)
+    if (x0 == warp) named_bar_sync(1, kWorkers);  // (the first round's loads are on their way)
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
       const int x = x0 + 8 * i, t = min(x, T * HP - 1) / HP, jh = min(x, T * HP - 1) % HP;

@@ -5,7 +5,8 @@ import torch
 
 import oracle
 from gated_delta_rule_81_b200 import gdn
-from test_gpu_tree import attn_case, attn_run, delta_case
+from gpu_helpers import OUT_TOL, out_error
+from test_gpu_tree import KEYS, attn_case, attn_run, delta_case, delta_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -84,6 +85,24 @@ def test_rope_amplitude_of_the_caller():
     rope.amplitude = 2.0
     got = gdn.qk_norm_rope(rope, q, positions=pos)[0]
     assert torch.equal(got[..., :64], 2 * want[..., :64]) and torch.equal(got[..., 64:], want[..., 64:])
+
+
+# ------------------------------------------------------------------ gdn_decode_tree
+
+@pytest.mark.parametrize("T,H_v", [(1, 2), (1, 3), (1, 7), (2, 3), (3, 2), (4, 2), (1, 8)])
+def test_decode_tree_fewer_rows_than_warps(T, H_v):
+    """Many sequences of trees so small that a CTA's warps outnumber its (node, value head) pairs: every repetition the same
+    bits, and the results of one sequence alone, whose value heads have a CTA each."""
+    N = 400
+    c = delta_case(N, T, 1, H_v, "chain", seed=81 + T)
+    out = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"])
+    for _ in range(40):
+        assert torch.equal(gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"]), out)
+    n = 40
+    sub = dict(c, rows=c["rows"][:n], slot=c["slot"][:n], inp={k: v[:n * T] if k in KEYS else v for k, v in c["inp"].items()})
+    assert out_error(out[:n * T], delta_ref(sub)["out"]) <= OUT_TOL
+    alone = gdn.decode_tree(c["s"], 1, T, c["parent"][:1].contiguous(), c["d_state"], c["d_conv"], state_slot=c["d_slot"][:1].contiguous())
+    assert torch.equal(alone, out[:T])
 
 
 # ------------------------------------------------------------------ gdn_decode_tree_commit
