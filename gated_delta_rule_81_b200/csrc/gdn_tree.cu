@@ -471,7 +471,8 @@ template <int NT>
 cudaError_t launch_nt(const TreeParams& p, int parts, cudaStream_t stream) {
   using C = TreeCfg<NT>;
   const int smem = C::smem(p.H_v / p.H_k / parts);
-  const cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit is the largest call's, the same in every call: two threads' calls may interleave here)
+  const cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(kMaxHeads));
   if (e != cudaSuccess) return e;
   decode_tree_kernel<NT><<<dim3(parts, p.H_k, p.N), C::kThreads, smem, stream>>>(p);
   return cudaGetLastError();

@@ -8,6 +8,7 @@
 namespace gdn {
 
 constexpr int kMaxNodes = GDN_MAX_TREE_NODES;
+constexpr int kMaxHeads = 8;          // value heads per key head
 constexpr int kDevErrCacheFull = 16;  // a sequence's KV cache has no row for a new token
 constexpr int kDevErrCacheLen = 32;   // a cache_len outside [0, cap]
 constexpr int kDevErrBadIndex = 128;  // a tree parent, an accepted node or a cache row outside its range

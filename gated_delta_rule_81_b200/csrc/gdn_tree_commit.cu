@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kCommitThreads, 4) tree_commit_kernel(TreePara
   __shared__ int path_s[kMaxNodes];
   __shared__ int len_s;
   __shared__ float red[kCommitPass];
-  __shared__ float alpha_s[kCommitPass * 8], beta_s[kCommitPass * 8];
+  __shared__ float alpha_s[kCommitPass * kMaxHeads], beta_s[kCommitPass * kMaxHeads];
 
   const int n_p16 = n_ch / 8;
   const bf16* cs_in = p.conv_in + static_cast<long long>(slot) * 3 * C_conv;
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kCommitThreads, 4) tree_commit_kernel(TreePara
       const long long tok = static_cast<long long>(n) * T + path_s[i0 + t];
       const float a = __bfloat162float(p.a[tok * p.sa + h]);
       const float b = __bfloat162float(p.b[tok * p.sb + h]);
-      alpha_s[t * 8 + jh] = expf(-expf(p.A_log[h]) * softplus_f(a));
-      beta_s[t * 8 + jh] = sigmoid_f(b);
+      alpha_s[t * kMaxHeads + jh] = expf(-expf(p.A_log[h]) * softplus_f(a));
+      beta_s[t * kMaxHeads + jh] = sigmoid_f(b);
     }
     cp_async_wait_all();
     __syncthreads();
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kCommitThreads, 4) tree_commit_kernel(TreePara
         float sk = (u_me ? d[1] : d[0]) + __shfl_xor_sync(0xffffffffu, u_me ? d[0] : d[1], 4);
         sk = sk + __shfl_xor_sync(0xffffffffu, sk, 2);
         sk = sk + __shfl_xor_sync(0xffffffffu, sk, 1);
-        const float al = alpha_s[t * 8 + jh], be = beta_s[t * 8 + jh];
+        const float al = alpha_s[t * kMaxHeads + jh], be = beta_s[t * kMaxHeads + jh];
         const int r_me = r0 + g + 4 * u_me;
         const float delta_me = be * (feat[t * n_kv + kD + r_me] - al * sk);
         const float2 al2 = make_float2(al, al);
@@ -317,8 +317,9 @@ cudaError_t launch_tree_commit(const TreeParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (static_cast<long long>(p.N) * p.H_k < n_sm) parts = G;
   const int smem = commit_smem(G / parts);
-  if (smem > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(tree_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+  // (the limit is the largest call's, the same in every call: two threads' calls may interleave here)
+  if (smem > 48 * 1024 && (e = cudaFuncSetAttribute(tree_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    commit_smem(kMaxHeads))) != cudaSuccess)
     return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(parts, p.H_k, p.N);

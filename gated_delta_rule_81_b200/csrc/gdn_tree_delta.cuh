@@ -7,7 +7,6 @@ namespace gdn {
 
 constexpr int kWorkers = 256;            // threads of warps 0-7
 constexpr int kVRow = 132;               // floats of a node's v (then o): lanes (g, c) read bank 8 c + g
-constexpr int kMaxHeads = 8;             // value heads per key head
 
 __device__ __forceinline__ void bar_arrive(int id, int n) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");

@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(kWorkers, 4) decode_tree_small_kernel(const __
 
 cudaError_t launch_decode_tree_small(const TreeParams& p, cudaStream_t stream) {
   const int smem = smem_bytes(p.H_v / p.H_k);
-  const cudaError_t e = cudaFuncSetAttribute(decode_tree_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit is the largest call's, the same in every call: two threads' calls may interleave here)
+  const cudaError_t e = cudaFuncSetAttribute(decode_tree_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem_bytes(kMaxHeads));
   if (e != cudaSuccess) return e;
   decode_tree_small_kernel<<<dim3(1, p.H_k, p.N), kWorkers, smem, stream>>>(p);
   return cudaGetLastError();

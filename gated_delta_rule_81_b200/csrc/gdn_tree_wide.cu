@@ -586,7 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tree_wide_kernel(const __g
 template <bool kAligned32>
 static cudaError_t launch(const TreeParams& p, int parts, cudaStream_t stream) {
   const int smem = smem_bytes(p.H_v / p.H_k / parts);
-  const cudaError_t e = cudaFuncSetAttribute(decode_tree_wide_kernel<kAligned32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit is the largest call's, the same in every call: two threads' calls may interleave here)
+  const cudaError_t e = cudaFuncSetAttribute(decode_tree_wide_kernel<kAligned32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             smem_bytes(kMaxHeads));
   if (e != cudaSuccess) return e;
   decode_tree_wide_kernel<kAligned32><<<dim3(parts, p.H_k, p.N), kThreads, smem, stream>>>(p);
   return cudaGetLastError();

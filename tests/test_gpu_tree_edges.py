@@ -1,4 +1,7 @@
-"""Tree calls at the edges of what they take: rows whose result has to be NaN."""
+"""Tree calls at the edges of what they take: rows whose result has to be NaN, trees of very few rows, calls that two threads make at once."""
+import ctypes
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -116,3 +119,85 @@ def test_decode_tree_commit_reads_the_path_s_query_rows():
     gdn.decode_tree_commit(c["s"], 1, T, c["parent"], acc, c["d_state"].clone(), C, state_slot=c["d_slot"])
     q = c["dev"]["q"].reshape(T, H_k * 128)
     assert torch.equal(C[int(c["slot"][0]), :, :H_k * 128], q[T - 3:])
+
+
+# ------------------------------------------------------------------ two host threads
+
+CALLERS = r"""
+#include <atomic>
+#include <functional>
+#include <thread>
+// a call whose arguments are all integers or addresses: each has its 64-bit slot (x86-64)
+struct Call { long long a[13]; };
+typedef int (*Fn)(long long, long long, long long, long long, long long, long long, long long, long long, long long, long long,
+                  long long, long long, long long);
+// two threads, each with its own call, `times` times; the first status that is not 0
+extern "C" int two_callers(Fn fn, const Call* calls, int times) {
+  std::atomic<int> bad{0}, ready{0};
+  auto run = [&](const Call& c) {
+    const long long* a = c.a;
+    ++ready;
+    while (ready < 2) {}
+    for (int i = 0; i < times && bad == 0; ++i) {
+      const int s = fn(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12]);
+      if (s != 0) bad = s;
+    }
+  };
+  std::thread x(run, std::cref(calls[0])), y(run, std::cref(calls[1]));
+  x.join();
+  y.join();
+  return bad;
+}
+"""
+
+
+class Call(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_longlong * 13)]
+
+    def __init__(self, *args):
+        super().__init__((ctypes.c_longlong * 13)(*args))
+
+
+@pytest.fixture(scope="module")
+def two_callers(tmp_path_factory):
+    d = tmp_path_factory.mktemp("callers")
+    (d / "callers.cpp").write_text(CALLERS)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-pthread", "-o", str(d / "callers.so"), str(d / "callers.cpp")],
+                   check=True)
+    lib = ctypes.CDLL(str(d / "callers.so"))
+
+    def run(name, a, b, times=20000):
+        torch.cuda.synchronize()
+        status = lib.two_callers(ctypes.cast(getattr(gdn.load(), name), ctypes.c_void_p), (Call * 2)(a, b), times)
+        torch.cuda.synchronize()
+        return status
+    return run
+
+
+def no_slots(N, T, H_v):
+    """A case whose slots are all out of range, so that the GPU's part of a call is short."""
+    c = delta_case(N, T, 1, H_v, "chain", seed=T)
+    c["d_slot"] = torch.full((N,), -1, dtype=torch.int32, device="cuda")
+    c["acc"] = torch.full((N,), T - 1, dtype=torch.int32, device="cuda")
+    c["out"] = torch.ones(N * T, H_v, 128, dtype=torch.bfloat16, device="cuda")
+    c["stream"] = torch.cuda.Stream()
+    return c
+
+
+@pytest.mark.parametrize("T", [5, 13, 30, 60])
+def test_two_threads_call_decode_tree_with_different_sizes(two_callers, T):
+    """Calls of one kernel with different amounts of shared memory (value heads per CTA), from two host threads at once:
+    none fails."""
+    cases = [no_slots(160, 5, 2), no_slots(160, 5, 8)] if T == 5 else [no_slots(1, T, 8), no_slots(160, T, 8)]
+    calls = [Call(ctypes.addressof(c["s"]), c["N"], T, c["parent"].data_ptr(), c["d_state"].data_ptr(), c["d_conv"].data_ptr(),
+                  c["d_slot"].data_ptr(), c["N"], c["out"].data_ptr(), 0, c["stream"].cuda_stream) for c in cases]
+    assert two_callers("gdn_decode_tree", *calls) == 0
+    assert all(bool((c["out"] == 0).all()) for c in cases)
+
+
+def test_two_threads_call_decode_tree_commit_with_different_sizes(two_callers):
+    cases = [no_slots(160, 3, 6), no_slots(160, 3, 8)]
+    calls = [Call(ctypes.addressof(c["s"]), c["N"], 3, c["parent"].data_ptr(), c["acc"].data_ptr(), c["d_state"].data_ptr(),
+                  c["d_state"].data_ptr(), c["d_conv"].data_ptr(), c["d_conv"].data_ptr(), c["d_slot"].data_ptr(), c["N"], 0,
+                  c["stream"].cuda_stream) for c in cases]
+    assert two_callers("gdn_decode_tree_commit", *calls) == 0
