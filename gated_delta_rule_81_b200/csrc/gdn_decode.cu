@@ -344,7 +344,9 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream, void* cons
   const int parts = decode_parts(p);
   const int smem = decode_smem(p.T, p.H_v / p.H_k / parts).total;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(gdn_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the limit is the largest call's, the same in every call: two threads' calls may interleave here
+    const cudaError_t e = cudaFuncSetAttribute(gdn_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               decode_smem(kMaxDecodeTokens, 8).total);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

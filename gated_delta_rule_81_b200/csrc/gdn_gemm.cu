@@ -283,6 +283,7 @@ int gemm_tile_width(int M, int N, int n_sm) {
 // the warp adds its lanes' sums with shuffles in a fixed order.  One bf16 rounding per output.
 constexpr int kGemvThreads = 256;
 constexpr int kGemvCols = 2;                                   // B rows (output columns) per warp
+constexpr int kGemvMaxSmem = 200 * 1024;                       // A's rows as fp32
 constexpr int kGemvColsPerCta = kGemvCols * kGemvThreads / 32;
 
 template <int MR>
@@ -347,7 +348,8 @@ template <int MR>
 cudaError_t launch_gemv(const bf16* A, long long lda, const bf16* B, long long ldb, bf16* C, long long ldc, int N,
                         int K, cudaStream_t stream) {
   const int smem = MR * K * 4;
-  cudaError_t e = cudaFuncSetAttribute(gemv_bf16_kernel<MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the largest call's, the same in every call: two threads' calls may interleave here
+  cudaError_t e = cudaFuncSetAttribute(gemv_bf16_kernel<MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemvMaxSmem);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>((N + kGemvColsPerCta - 1) / kGemvColsPerCta);
   gemv_bf16_kernel<MR><<<grid, kGemvThreads, smem, stream>>>(A, lda, B, ldb, C, ldc, N, K);
@@ -357,7 +359,7 @@ cudaError_t launch_gemv(const bf16* A, long long lda, const bf16* B, long long l
 cudaError_t launch_gemm_bf16(const bf16* A, long long lda, const bf16* B, long long ldb, bf16* C, long long ldc,
                              int M, int N, int K, int* err, cudaStream_t stream) {
   // a few rows: stream the weights once (A's rows in shared memory, MR * K * 4 bytes)
-  if (M <= kGemvMaxM && static_cast<long long>(M) * K * 4 <= 200 * 1024) {
+  if (M <= kGemvMaxM && static_cast<long long>(M) * K * 4 <= kGemvMaxSmem) {
     switch (M) {
       case 1: return launch_gemv<1>(A, lda, B, ldb, C, ldc, N, K, stream);
       case 2: return launch_gemv<2>(A, lda, B, ldb, C, ldc, N, K, stream);

@@ -201,3 +201,19 @@ def test_two_threads_call_decode_tree_commit_with_different_sizes(two_callers):
                   c["d_state"].data_ptr(), c["d_conv"].data_ptr(), c["d_conv"].data_ptr(), c["d_slot"].data_ptr(), c["N"], 0,
                   c["stream"].cuda_stream) for c in cases]
     assert two_callers("gdn_decode_tree_commit", *calls) == 0
+
+def test_two_threads_call_decode_multi_with_different_sizes(two_callers):
+    cases = [no_slots(160, 8, 6), no_slots(160, 8, 8)]
+    calls = [Call(ctypes.addressof(c["s"]), c["N"], 8, c["d_state"].data_ptr(), c["d_conv"].data_ptr(), c["d_slot"].data_ptr(),
+                  c["N"], c["out"].data_ptr(), 0, c["stream"].cuda_stream) for c in cases]
+    assert two_callers("gdn_decode_multi", *calls) == 0
+
+
+def test_two_threads_call_gemm_of_few_rows_with_different_sizes(two_callers):
+    """A layer's two projections of up to 4 rows, as a tree of few nodes makes them, on two threads."""
+    mats, calls = [], []
+    for K in (64, 8192):
+        a, b, out = (torch.zeros(*s, dtype=torch.bfloat16, device="cuda") for s in ((4, K), (32, K), (4, 32)))
+        mats.append((a, b, out, torch.cuda.Stream()))
+        calls.append(Call(a.data_ptr(), K, b.data_ptr(), K, out.data_ptr(), 32, 4, 32, K, 0, mats[-1][3].cuda_stream))
+    assert two_callers("gdn_gemm_bf16", *calls) == 0
