@@ -701,6 +701,12 @@ def attn_tree_commit(k_tree, v_tree, T: int, parent, accepted, k_cache, v_cache,
     return cache_len_out
 
 
+def _want_slots(N, slots, state_slot):
+    """Without slots sequence n has slot n, so the pool needs N (the layer's entry points are not told how many it has)."""
+    if state_slot is None and slots < N:
+        raise ValueError(f"{N} sequences need {N} slots (or state_slot), not {slots}")
+
+
 def layer_tree_workspace(L: GdnLayer, N: int, T: int, device):
     """The workspace of layer_decode_tree, kept until layer_tree_commit."""
     return torch.empty(int(load().gdn_layer_tree_workspace_size(L.H_k, L.H_v, N, T)), dtype=torch.uint8, device=device)
@@ -711,6 +717,7 @@ def layer_decode_tree(L: GdnLayer, N: int, T: int, parent, x, state, conv_state,
     """gdn_layer_decode_tree: x [N*T][hidden] -> y; state and conv_state are read, `workspace` keeps the projection
     for layer_tree_commit.  Returns y."""
     slots, dev = _want_pool(L.H_k, L.H_v, state, conv_state)
+    _want_slots(N, slots, state_slot)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
     if y is None:
@@ -726,6 +733,7 @@ def layer_tree_commit(L: GdnLayer, N: int, T: int, parent, accepted, state, conv
     """gdn_layer_tree_commit: state and conv_state advanced in place along the accepted paths of the
     layer_decode_tree call that left `workspace`."""
     slots, dev = _want_pool(L.H_k, L.H_v, state, conv_state)
+    _want_slots(N, slots, state_slot)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("accepted", accepted, torch.int32, (N,), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)

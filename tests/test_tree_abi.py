@@ -6,6 +6,7 @@ import os
 
 import numpy as np
 import pytest
+import torch
 
 import oracle
 from gated_delta_rule_81_b200 import build, gdn
@@ -238,6 +239,27 @@ def test_layer_tree_sizes_and_refusals(lib):
     assert lib.gdn_layer_tree_commit(ctypes.byref(L), 2, 4, PARENT, ACC, 32 << 36, CONV, None, 2, 32 << 36, need, None, None) == ALIAS
     assert lib.gdn_layer_tree_commit(ctypes.byref(L), 2, 4, PARENT, ACC, STATE, CONV, None, 2, 32 << 36, 5, None, None) == WORKSPACE
     assert lib.gdn_attn_layer_tree_commit(2, 4, PARENT, ACC, STATE, CONV, 9, SLOT, 32 << 36, 5, None, None) == WORKSPACE
+
+
+def cpu_layer(hidden=64, H_k=1, H_v=2):
+    L = gdn.GdnLayer()
+    L.H_k, L.H_v, L.hidden = H_k, H_v, hidden
+    return L
+
+
+def cpu_pool(slots, H_k=1, H_v=2):
+    return torch.zeros(slots, H_v, 128, 128), torch.zeros(slots, 3, (2 * H_k + H_v) * 128, dtype=torch.bfloat16)
+
+
+def test_layer_calls_refuse_a_pool_of_fewer_slots_than_sequences(lib):
+    """Without state_slot sequence n reads (and at the commit writes) slot n."""
+    L, N, T = cpu_layer(), 3, 2
+    x, ws = torch.zeros(N * T, 64, dtype=torch.bfloat16), torch.zeros(1 << 16, dtype=torch.uint8)
+    acc = torch.zeros(N, dtype=torch.int32)
+    with pytest.raises(ValueError, match="slots"):
+        gdn.layer_decode_tree(L, N, T, None, x, *cpu_pool(2), ws)
+    with pytest.raises(ValueError, match="slots"):
+        gdn.layer_tree_commit(L, N, T, None, acc, *cpu_pool(2), ws)
 
 
 def test_tree_oracle_paths():
