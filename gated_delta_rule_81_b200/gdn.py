@@ -524,6 +524,30 @@ def _want(name, t, dtype, shape=None, device=None):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
+def _want_err(err, device):
+    if err is not None and (err.dtype is not torch.int32 or err.numel() < 1 or err.device != device):
+        raise ValueError(f"err must be an int32 on {device}, not {err.dtype} on {err.device}")
+
+
+def _workspace_bytes(workspace, device):
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
+def _matrix(name, t, rows, cols, device):
+    """Row stride of a bf16 matrix of at least rows x cols, of which those are used."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be bf16, not {t.dtype}")
+    if t.dim() != 2 or t.shape[0] < rows or t.shape[1] < cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}][{cols}] with rows side by side, not {tuple(t.shape)} by {t.stride()}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.stride(0) if rows > 1 else cols
+
+
 def _rows(name, t, tokens, heads, dim, device):
     """Token stride of a bf16 [tokens][heads][dim] tensor whose tokens' heads lie side by side."""
     shape, stride = t.shape, t.stride()
@@ -557,6 +581,7 @@ def decode_tree(inp: GdnInputs, N: int, T: int, parent, state, conv_state, state
         out = torch.empty((N * T, inp.H_v, HEAD_DIM), dtype=torch.bfloat16, device=dev)
     else:
         _want("out", out, torch.bfloat16, (N * T, inp.H_v, HEAD_DIM), dev)
+    _want_err(err, dev)
     _run_on(dev, "gdn_decode_tree", inp, N, T, _addr(parent), _addr(state), _addr(conv_state),
             _addr(state_slot), slots, _addr(out), _addr(err))
     return out
@@ -579,6 +604,7 @@ def decode_tree_commit(inp: GdnInputs, N: int, T: int, parent, accepted, state, 
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("accepted", accepted, torch.int32, (N,), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
+    _want_err(err, dev)
     _run_on(dev, "gdn_decode_tree_commit", inp, N, T, _addr(parent), _addr(accepted), _addr(state),
             _addr(state_out), _addr(conv_state), _addr(conv_out), _addr(state_slot), slots, _addr(err))
     return state_out, conv_out
@@ -637,6 +663,7 @@ def qk_norm_rope(rope: GdnRope, q, k=None, v=None, *, q_norm_w=None, k_norm_w=No
     _want("k_norm_w", k_norm_w, torch.bfloat16, (D,), dev)
     _want("positions", positions, torch.int32, (n_tok,), dev)
     _want("rows", rows, torch.int64, (n_tok,), dev)
+    _want_err(err, dev)
     _run_on(dev, "gdn_qk_norm_rope", rope, n_tok, H_q, H_kv, _addr(q), ld_q, _addr(k), ld_k, _addr(v), ld_v,
             _addr(q_norm_w), _addr(k_norm_w), _addr(positions), _addr(rows), n_rows,
             None if q is None else q_out.data_ptr(), ld_qo, None if k is None else k_out.data_ptr(), ld_ko,
@@ -669,9 +696,11 @@ def attention_tree(q_hat, k_tree, v_tree, k_cache, v_cache, cache_len, parent=No
         _want("out", out, torch.bfloat16, (n_tok, H_q * D), dev)
     if workspace is None:
         workspace = torch.empty(attention_tree_workspace_size(H_q, H_kv, D, N, T), dtype=torch.uint8, device=dev)
+    nbytes = _workspace_bytes(workspace, dev)
+    _want_err(err, dev)
     _run_on(dev, "gdn_attention_tree", _addr(q_hat), ld_q, _addr(k_tree), ld_kt, _addr(v_tree), ld_vt, _addr(k_cache),
             _addr(v_cache), cap, _addr(cache_len), _addr(parent), _addr(g), ld_g, H_q, H_kv, D,
-            D ** -0.5 if scale is None else scale, N, T, _addr(out), _addr(workspace), workspace.numel(), _addr(err))
+            D ** -0.5 if scale is None else scale, N, T, _addr(out), _addr(workspace), nbytes, _addr(err))
     return out
 
 
@@ -696,6 +725,7 @@ def attn_tree_commit(k_tree, v_tree, T: int, parent, accepted, k_cache, v_cache,
         _want("cache_len_out", cache_len_out, torch.int32, (N,), dev)
     ld_kt = _rows("k_tree", k_tree, N * T, H_kv, D, dev)
     ld_vt = _rows("v_tree", v_tree, N * T, H_kv, D, dev)
+    _want_err(err, dev)
     _run_on(dev, "gdn_attn_tree_commit", _addr(k_tree), ld_kt, _addr(v_tree), ld_vt, H_kv, D, N, T, _addr(parent),
             _addr(accepted), _addr(k_cache), _addr(v_cache), cap, _addr(cache_len), _addr(cache_len_out), _addr(err))
     return cache_len_out
@@ -720,10 +750,14 @@ def layer_decode_tree(L: GdnLayer, N: int, T: int, parent, x, state, conv_state,
     _want_slots(N, slots, state_slot)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
+    ldx = _matrix("x", x, N * T, L.hidden, dev)
     if y is None:
         y = torch.empty(N * T, L.hidden, dtype=torch.bfloat16, device=dev)
-    _run_on(dev, "gdn_layer_decode_tree", L, N, T, _addr(parent), _addr(x), x.stride(0), _addr(state),
-            _addr(conv_state), _addr(state_slot), slots, _addr(y), y.stride(0), _addr(workspace), workspace.numel(),
+    ldy = _matrix("y", y, N * T, L.hidden, dev)
+    nbytes = _workspace_bytes(workspace, dev)
+    _want_err(err, dev)
+    _run_on(dev, "gdn_layer_decode_tree", L, N, T, _addr(parent), _addr(x), ldx, _addr(state),
+            _addr(conv_state), _addr(state_slot), slots, _addr(y), ldy, _addr(workspace), nbytes,
             _addr(err))
     return y
 
@@ -737,8 +771,10 @@ def layer_tree_commit(L: GdnLayer, N: int, T: int, parent, accepted, state, conv
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("accepted", accepted, torch.int32, (N,), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
+    nbytes = _workspace_bytes(workspace, dev)
+    _want_err(err, dev)
     _run_on(dev, "gdn_layer_tree_commit", L, N, T, _addr(parent), _addr(accepted), _addr(state),
-            _addr(conv_state), _addr(state_slot), slots, _addr(workspace), workspace.numel(), _addr(err))
+            _addr(conv_state), _addr(state_slot), slots, _addr(workspace), nbytes, _addr(err))
 
 
 def attn_layer_tree_workspace(N: int, T: int, device):
@@ -760,10 +796,14 @@ def attn_layer_decode_tree(L: GdnAttnLayer, N: int, T: int, parent, x, k_cache, 
     nodes' keys and values for attn_layer_tree_commit.  Returns y."""
     dev, cap = _want_attn_cache(N, k_cache, v_cache, cache_len)
     _want("parent", parent, torch.int32, (N, T), dev)
+    ldx = _matrix("x", x, N * T, L.hidden, dev)
     if y is None:
         y = torch.empty(N * T, L.hidden, dtype=torch.bfloat16, device=dev)
-    _run_on(dev, "gdn_attn_layer_decode_tree", L, N, T, _addr(parent), _addr(x), x.stride(0), _addr(k_cache),
-            _addr(v_cache), cap, _addr(cache_len), _addr(y), y.stride(0), _addr(workspace), workspace.numel(), _addr(err))
+    ldy = _matrix("y", y, N * T, L.hidden, dev)
+    nbytes = _workspace_bytes(workspace, dev)
+    _want_err(err, dev)
+    _run_on(dev, "gdn_attn_layer_decode_tree", L, N, T, _addr(parent), _addr(x), ldx, _addr(k_cache),
+            _addr(v_cache), cap, _addr(cache_len), _addr(y), ldy, _addr(workspace), nbytes, _addr(err))
     return y
 
 
@@ -772,8 +812,10 @@ def attn_layer_tree_commit(N: int, T: int, parent, accepted, k_cache, v_cache, c
     dev, cap = _want_attn_cache(N, k_cache, v_cache, cache_len)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("accepted", accepted, torch.int32, (N,), dev)
+    nbytes = _workspace_bytes(workspace, dev)
+    _want_err(err, dev)
     _run_on(dev, "gdn_attn_layer_tree_commit", N, T, _addr(parent), _addr(accepted), _addr(k_cache), _addr(v_cache), cap,
-            _addr(cache_len), _addr(workspace), workspace.numel(), _addr(err))
+            _addr(cache_len), _addr(workspace), nbytes, _addr(err))
 
 
 def status_string(status: int) -> str:

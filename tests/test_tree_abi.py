@@ -262,6 +262,58 @@ def test_layer_calls_refuse_a_pool_of_fewer_slots_than_sequences(lib):
         gdn.layer_tree_commit(L, N, T, None, acc, *cpu_pool(2), ws)
 
 
+def bf(*shape, device="cpu"):
+    return torch.zeros(*shape, dtype=torch.bfloat16, device=device)
+
+
+BAD_X = [  # of the wrong type, on another device, too few rows, too narrow, transposed, of another rank
+    (torch.zeros(6, 64), TypeError), (bf(6, 64, device="meta"), ValueError), (bf(5, 64), ValueError), (bf(6, 63), ValueError),
+    (bf(64, 6).T, ValueError), (bf(6 * 64), ValueError)]
+
+
+@pytest.mark.parametrize("bad,error", BAD_X, ids=["fp32", "device", "rows", "width", "transposed", "rank"])
+@pytest.mark.parametrize("name", ["x", "y"])
+@pytest.mark.parametrize("attn", [False, True])
+def test_layer_calls_check_their_matrices(lib, bad, error, name, attn):
+    L, N, T = cpu_layer(), 3, 2
+    m = {"x": bf(6, 64), "y": bf(6, 64), name: bad}
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    with pytest.raises(error, match=name):
+        if attn:
+            gdn.attn_layer_decode_tree(L, N, T, None, m["x"], bf(N, 5, 4, 256), bf(N, 5, 4, 256), torch.zeros(N, dtype=torch.int32), ws,
+                                       y=m["y"])
+        else:
+            gdn.layer_decode_tree(L, N, T, None, m["x"], *cpu_pool(N), ws, y=m["y"])
+
+
+BAD_WS = [torch.zeros(1 << 16, dtype=torch.uint8, device="meta"), torch.zeros(2, 1 << 16, dtype=torch.uint8)[:, ::2]]
+BAD_ERR = [torch.zeros(1, dtype=torch.int64), torch.zeros(1, dtype=torch.int32, device="meta"), torch.zeros(0, dtype=torch.int32)]
+
+
+@pytest.mark.parametrize("what,bad", [("workspace", w) for w in BAD_WS] + [("err", e) for e in BAD_ERR])
+def test_tree_calls_check_their_workspace_and_error_word(lib, what, bad):
+    L, N, T = cpu_layer(), 1, 2
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    ws, err = (bad, None) if what == "workspace" else (torch.zeros(1 << 16, dtype=torch.uint8), bad)
+    S, C = cpu_pool(N)
+    kc, vc, n = bf(N, 5, 4, 256), bf(N, 5, 4, 256), i32(N)
+    kt = bf(N * T, 4, 256)
+    calls = [lambda: gdn.layer_decode_tree(L, N, T, None, bf(2, 64), S, C, ws, err=err),
+             lambda: gdn.layer_tree_commit(L, N, T, None, i32(N), S, C, ws, err=err),
+             lambda: gdn.attn_layer_decode_tree(L, N, T, None, bf(2, 64), kc, vc, n, ws, err=err),
+             lambda: gdn.attn_layer_tree_commit(N, T, None, i32(N), kc, vc, n, ws, err=err),
+             lambda: gdn.attention_tree(bf(2, 24, 256), kt, kt, kc, vc, n, T=T, workspace=ws, err=err)]
+    if what == "err":
+        inp = fake_inputs(1, 2)
+        calls += [lambda: gdn.decode_tree(inp, N, T, None, S, C, err=err),
+                  lambda: gdn.decode_tree_commit(inp, N, T, None, i32(N), S, C, err=err),
+                  lambda: gdn.qk_norm_rope(gdn.make_rope(256), kt, err=err),
+                  lambda: gdn.attn_tree_commit(kt, kt, T, None, i32(N), kc, vc, n, err=err)]
+    for call in calls:
+        with pytest.raises(ValueError, match=what):
+            call()
+
+
 def test_tree_oracle_paths():
     assert oracle.tree.paths([-1, 0, -1, 1, -2, 4, 2]) == [[0], [0, 1], [2], [0, 1, 3], [], [], [2, 6]]
     assert oracle.tree.paths([0, -1]) == [[], [1]]
