@@ -40,6 +40,8 @@ class GdnInputs(ctypes.Structure):
         ("events", ctypes.c_void_p),
         ("schedule", ctypes.c_int),
     ]
+    tokens = devices = None  # of the tensors, where make_inputs has filled it
+
 
 class GdnLayer(ctypes.Structure):
     """gdn_layer: the weights of one delta-rule layer (device pointers)."""
@@ -51,6 +53,7 @@ class GdnLayer(ctypes.Structure):
         ("scale", ctypes.c_float), ("schedule", ctypes.c_int),
         ("events", ctypes.c_void_p),
     ]
+    devices = None  # of the tensors, where make_layer has filled it
 
 
 class GdnAttnLayer(ctypes.Structure):
@@ -62,6 +65,7 @@ class GdnAttnLayer(ctypes.Structure):
         ("hidden", ctypes.c_int),
         ("events", ctypes.c_void_p),
     ]
+    devices = None  # of the tensors, where make_attn_layer has filled it
 
 
 ROPE_MAX_HEAD_DIM = 256
@@ -225,6 +229,8 @@ def make_inputs(q, k, v, a, b, z, conv_w, A_log, norm_w, scale=1.0, schedule=SCH
     s.conv_w, s.A_log, s.norm_w = conv_w.data_ptr(), A_log.data_ptr(), norm_w.data_ptr()
     s.H_k, s.H_v, s.scale = int(H_k), int(H_v), float(scale)
     s.schedule = int(schedule)
+    s.tokens = min(t.shape[0] for t in (q, k, v, a, b, z))
+    s.devices = {t.device for t in (q, k, v, a, b, z, conv_w, A_log, norm_w)}
     return s
 
 
@@ -386,6 +392,7 @@ def make_layer(w_in, w_out, conv_w, A_log, norm_w, H_k, H_v, scale=1.0, schedule
     L.conv_w, L.A_log, L.norm_w = conv_w.data_ptr(), A_log.data_ptr(), norm_w.data_ptr()
     L.H_k, L.H_v, L.hidden = int(H_k), int(H_v), int(w_in.shape[1])
     L.scale, L.schedule = float(scale), int(schedule)
+    L.devices = {t.device for t in (w_in, w_out, conv_w, A_log, norm_w)}
     return L
 
 
@@ -439,6 +446,7 @@ def make_attn_layer(w_in, w_out, q_norm_w, k_norm_w) -> GdnAttnLayer:
     L.w_out, L.ld_w_out = w_out.data_ptr(), w_out.stride(0)
     L.q_norm_w, L.k_norm_w = q_norm_w.data_ptr(), k_norm_w.data_ptr()
     L.hidden = int(w_in.shape[1])
+    L.devices = {t.device for t in (w_in, w_out, q_norm_w, k_norm_w)}
     return L
 
 
@@ -524,6 +532,14 @@ def _want(name, t, dtype, shape=None, device=None):
         raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
+def _want_made(made, device, tokens=0):
+    """The tensors of an input descriptor or a layer, as far as it knows them."""
+    if made.devices is not None and made.devices != {device}:
+        raise ValueError(f"the {type(made).__name__}'s tensors are on {sorted(map(str, made.devices))}, not on {device}")
+    if tokens > 0 and made.tokens is not None and made.tokens < tokens:
+        raise ValueError(f"the inputs hold {made.tokens} tokens, not {tokens}")
+
+
 def _want_err(err, device):
     if err is not None and (err.dtype is not torch.int32 or err.numel() < 1 or err.device != device):
         raise ValueError(f"err must be an int32 on {device}, not {err.dtype} on {err.device}")
@@ -575,6 +591,7 @@ def decode_tree(inp: GdnInputs, N: int, T: int, parent, state, conv_state, state
     parent: device int32 [N][T] (-1 a child of the last committed token, an earlier node, or -2 for no
     node), None for a chain.  state and conv_state (the pools) are read.  Returns out [N*T][H_v][128] bf16."""
     slots, dev = _want_pool(inp.H_k, inp.H_v, state, conv_state)
+    _want_made(inp, dev, N * T)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
     if out is None:
@@ -593,6 +610,7 @@ def decode_tree_commit(inp: GdnInputs, N: int, T: int, parent, accepted, state, 
     (device int32 [N], -1: none), in place unless state_out / conv_out are given.  `inp`'s q, k, v, a and b hold what
     they held at decode_tree (the last raw rows become the conv state).  Returns both."""
     slots, dev = _want_pool(inp.H_k, inp.H_v, state, conv_state)
+    _want_made(inp, dev, N * T)
     if state_out is None:
         state_out = state
     else:
@@ -747,6 +765,7 @@ def layer_decode_tree(L: GdnLayer, N: int, T: int, parent, x, state, conv_state,
     """gdn_layer_decode_tree: x [N*T][hidden] -> y; state and conv_state are read, `workspace` keeps the projection
     for layer_tree_commit.  Returns y."""
     slots, dev = _want_pool(L.H_k, L.H_v, state, conv_state)
+    _want_made(L, dev)
     _want_slots(N, slots, state_slot)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("state_slot", state_slot, torch.int32, (N,), dev)
@@ -767,6 +786,7 @@ def layer_tree_commit(L: GdnLayer, N: int, T: int, parent, accepted, state, conv
     """gdn_layer_tree_commit: state and conv_state advanced in place along the accepted paths of the
     layer_decode_tree call that left `workspace`."""
     slots, dev = _want_pool(L.H_k, L.H_v, state, conv_state)
+    _want_made(L, dev)
     _want_slots(N, slots, state_slot)
     _want("parent", parent, torch.int32, (N, T), dev)
     _want("accepted", accepted, torch.int32, (N,), dev)
@@ -795,6 +815,7 @@ def attn_layer_decode_tree(L: GdnAttnLayer, N: int, T: int, parent, x, k_cache, 
     """gdn_attn_layer_decode_tree: x [N*T][hidden] -> y; the caches and cache_len are read, `workspace` keeps the
     nodes' keys and values for attn_layer_tree_commit.  Returns y."""
     dev, cap = _want_attn_cache(N, k_cache, v_cache, cache_len)
+    _want_made(L, dev)
     _want("parent", parent, torch.int32, (N, T), dev)
     ldx = _matrix("x", x, N * T, L.hidden, dev)
     if y is None:

@@ -314,6 +314,38 @@ def test_tree_calls_check_their_workspace_and_error_word(lib, what, bad):
             call()
 
 
+def cpu_inputs(tokens, H_k=1, H_v=2, short=None, away=None):
+    """A descriptor of CPU tensors; one may hold fewer tokens, one may lie elsewhere."""
+    n = {k: tokens - (k == short) for k in ("q", "k", "v", "a", "b", "z")}
+    dev = lambda k: "meta" if k == away else "cpu"
+    w = {"q": H_k * 128, "k": H_k * 128, "v": H_v * 128, "a": H_v, "b": H_v, "z": H_v * 128}
+    return gdn.make_inputs(*(bf(n[k], w[k], device=dev(k)) for k in ("q", "k", "v", "a", "b", "z")),
+                           bf((2 * H_k + H_v) * 128, 4, device=dev("conv_w")), torch.zeros(H_v, device=dev("A_log")), bf(128))
+
+
+@pytest.mark.parametrize("bad,words", [({"short": k}, "5 tokens, not 6") for k in ("q", "v", "a", "z")] +
+                         [({"away": k}, "meta") for k in ("k", "b", "conv_w", "A_log")])
+def test_decode_tree_calls_check_the_descriptor_s_tensors(lib, bad, words):
+    """The descriptor holds addresses alone: how many tokens there are, and where, is kept beside them."""
+    inp = cpu_inputs(6, **bad)
+    with pytest.raises(ValueError, match=words):
+        gdn.decode_tree(inp, 3, 2, None, *cpu_pool(3))
+    with pytest.raises(ValueError, match=words):
+        gdn.decode_tree_commit(inp, 3, 2, None, torch.zeros(3, dtype=torch.int32), *cpu_pool(3))
+
+
+def test_layer_tree_calls_check_the_layer_s_device(lib):
+    ws, acc = torch.zeros(1 << 16, dtype=torch.uint8), torch.zeros(1, dtype=torch.int32)
+    L = gdn.make_layer(bf(64 * 16, 64, device="meta"), bf(64, 256), bf(512, 4), torch.zeros(2), bf(128), 1, 2)
+    with pytest.raises(ValueError, match="meta"):
+        gdn.layer_decode_tree(L, 1, 2, None, bf(2, 64), *cpu_pool(1), ws)
+    with pytest.raises(ValueError, match="meta"):
+        gdn.layer_tree_commit(L, 1, 2, None, acc, *cpu_pool(1), ws)
+    L = gdn.make_attn_layer(bf(gdn.ATTN_N_IN, 64), bf(64, 24 * 256), bf(256), bf(256, device="meta"))
+    with pytest.raises(ValueError, match="meta"):
+        gdn.attn_layer_decode_tree(L, 1, 2, None, bf(2, 64), bf(1, 5, 4, 256), bf(1, 5, 4, 256), acc, ws)
+
+
 def test_tree_oracle_paths():
     assert oracle.tree.paths([-1, 0, -1, 1, -2, 4, 2]) == [[0], [0, 1], [2], [0, 1, 3], [], [], [2, 6]]
     assert oracle.tree.paths([0, -1]) == [[], [1]]
