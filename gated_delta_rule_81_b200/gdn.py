@@ -575,7 +575,9 @@ def _rows(name, t, tokens, heads, dim, device):
         raise ValueError(f"{name} must have its heads side by side, not strides {stride}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return stride[0] if tokens > 1 else max(stride[0], heads * dim)
+    if tokens <= 1 and (stride[0] < heads * dim or stride[0] % 8):  # a single row's stride may be anything
+        return heads * dim
+    return stride[0]
 
 
 def _want_pool(H_k, H_v, state, conv_state):

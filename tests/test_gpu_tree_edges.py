@@ -217,3 +217,24 @@ def test_two_threads_call_gemm_of_few_rows_with_different_sizes(two_callers):
         mats.append((a, b, out, torch.cuda.Stream()))
         calls.append(Call(a.data_ptr(), K, b.data_ptr(), K, out.data_ptr(), 32, 4, 32, K, 0, mats[-1][3].cuda_stream))
     assert two_callers("gdn_gemm_bf16", *calls) == 0
+
+
+# ------------------------------------------------------------------ bindings
+
+def test_single_rows_of_any_stride():
+    """One token: the stride of its (only) row means nothing."""
+    D, H = 128, 2
+    buf = torch.randn(H * D + 1, device="cuda").to(torch.bfloat16)
+    x = buf.as_strided((1, H, D), (H * D + 1, D, 1))
+    rope = gdn.make_rope(D)
+    want = gdn.qk_norm_rope(rope, x.contiguous(), x.contiguous(), x.contiguous())
+    got = gdn.qk_norm_rope(rope, x, x, x)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    c = attn_case(1, 1, 2, 1, D, [70], "chain", seed=91)
+    want = attn_run(c)
+    odd = {}
+    for k in ("q", "kt", "vt", "g"):
+        h = c[k].shape[1]
+        odd[k] = torch.empty(h * D + 1, dtype=torch.bfloat16, device="cuda").as_strided((1, h, D), (h * D + 1, D, 1))
+        odd[k].copy_(c[k])
+    assert torch.equal(attn_run(c | odd), want)
