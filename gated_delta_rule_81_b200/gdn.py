@@ -699,7 +699,7 @@ def attention_tree(q_hat, k_tree, v_tree, k_cache, v_cache, cache_len, parent=No
     Returns out [N*T][H_q*D] bf16."""
     N, cap, H_kv, D = k_cache.shape
     dev = k_cache.device
-    T = T if T is not None else parent.shape[1] if parent is not None else q_hat.shape[0] // max(N, 1)
+    T = T if T is not None else parent.shape[1] if parent is not None else q_hat.shape[0] // N if N else 1
     H_q = q_hat.shape[1]
     _want("k_cache", k_cache, torch.bfloat16, None, dev)
     _want("v_cache", v_cache, torch.bfloat16, k_cache.shape, dev)

@@ -238,3 +238,12 @@ def test_single_rows_of_any_stride():
         odd[k] = torch.empty(h * D + 1, dtype=torch.bfloat16, device="cuda").as_strided((1, h, D), (h * D + 1, D, 1))
         odd[k].copy_(c[k])
     assert torch.equal(attn_run(c | odd), want)
+
+
+def test_attention_tree_of_no_sequences():
+    """A batch of no sequences, with and without a tree: no rows."""
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+    for parent in (None, torch.empty(0, 5, dtype=torch.int32, device="cuda")):
+        out = gdn.attention_tree(e(0, 4, 128), e(0, 2, 128), e(0, 2, 128), e(0, 9, 2, 128), e(0, 9, 2, 128),
+                                 torch.empty(0, dtype=torch.int32, device="cuda"), parent)
+        assert out.shape == (0, 512)
