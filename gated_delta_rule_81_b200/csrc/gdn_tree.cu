@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
       const int jh = x / TP, t = x % TP, h = hv0 + jh;
       float gl = 0.f, be = 0.f;
       if (t < T && tree.mask[t]) {
-        gl = -expf(p.A_log[h]) * softplus_f(__bfloat162float(p.a[(tok0 + t) * p.sa + h]));
+        gl = log_decay(-expf(p.A_log[h]), __bfloat162float(p.a[(tok0 + t) * p.sa + h]));
         be = sigmoid_f(__bfloat162float(p.b[(tok0 + t) * p.sb + h]));
       }
       g_s[jh][t] = gl;

@@ -63,6 +63,14 @@ __device__ __forceinline__ void zero_rows(const TreeParams& p, int n, int T, int
   }
 }
 
+// A node's log decay from its logit, rate = -e^{A_log}; not below -128, whose decay is zero in fp32 like every smaller one.  Without
+// the limit one infinite or huge term takes the path sums of all nodes behind it (infinite, or too large to hold the other terms)
+// and with them the differences that are the decays between those nodes.  NaN stays NaN.
+__device__ __forceinline__ float log_decay(float rate, float a) {
+  const float g = rate * softplus_f(a);
+  return g < -128.f ? -128.f : g;
+}
+
 // Sums of log decays up each node's path, by pointer doubling: lane l holds nodes l and l + 32, `up` their parents (-1 at a root
 // and for absent nodes).
 __device__ __forceinline__ void path_sums(double (&acc)[2], int (&up)[2]) {

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kWorkers, 4) decode_tree_small_kernel(const __
   cp_async_wait_all();
   __syncthreads();
   if (warp < HP && lane < T && tree.mask[lane]) {
-    gl = -expf(p.A_log[hv0 + warp]) * softplus_f(__bfloat162float(p.a[(tok0 + lane) * p.sa + hv0 + warp]));
+    gl = log_decay(-expf(p.A_log[hv0 + warp]), __bfloat162float(p.a[(tok0 + lane) * p.sa + hv0 + warp]));
     be = sigmoid_f(__bfloat162float(p.b[(tok0 + lane) * p.sb + hv0 + warp]));
   }
   {

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_tree_wide_kernel(const __g
       const int t = lane + 32 * e;
       const bool there = t < T && tree.mask[t];
       up[e] = there ? tree.parent[t] : -1;
-      acc[e] = there ? static_cast<double>(rate * softplus_f(__bfloat162float(a_raw[e]))) : 0.0;
+      acc[e] = there ? static_cast<double>(log_decay(rate, __bfloat162float(a_raw[e]))) : 0.0;
       sh.beta[gate_head][t] = there ? sigmoid_f(__bfloat162float(b_raw[e])) : 0.f;
     }
     path_sums(acc, up);

@@ -108,6 +108,26 @@ def test_decode_tree_fewer_rows_than_warps(T, H_v):
     assert torch.equal(alone, out[:T])
 
 
+@pytest.mark.parametrize("value", [float("inf"), 3e38, 1e20, 1e9, 300.0, 120.0])
+@pytest.mark.parametrize("N,T,H_k,H_v", [(1, 7, 2, 6), (90, 7, 2, 6), (1, 16, 2, 6), (2, 32, 2, 4), (1, 40, 2, 6), (90, 61, 1, 3)])
+def test_decode_tree_gate_that_forgets_everything(N, T, H_k, H_v, value):
+    """A decay logit so large that the node's decay is zero: its descendants go on from an empty state, as decoding the
+    path token by token does."""
+    c = delta_case(N, T, H_k, H_v, "chain", seed=61 + T, a_mean=-2.0)
+    at = T // 3
+    tok = torch.arange(N) * T + at
+    for x in (c["inp"]["a"], c["dev"]["a"]):
+        x[tok.to(x.device)] = value
+    out = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"])
+    assert bool(torch.isfinite(out).all())
+    n = min(N, 2)
+    sub = dict(c, rows=c["rows"][:n], slot=c["slot"][:n], inp={k: v[:n * T] if k in KEYS else v for k, v in c["inp"].items()})
+    sl = sub["slot"].long()
+    ref = oracle.tree.mixer_tree(sub["inp"], sub["rows"], c["state"][sl], c["conv"][sl])["out"]
+    assert np.isfinite(ref).all()
+    assert out_error(out[:n * T], ref) <= OUT_TOL
+
+
 # ------------------------------------------------------------------ gdn_decode_tree_commit
 
 def test_decode_tree_commit_reads_the_path_s_query_rows():
