@@ -45,6 +45,7 @@ constexpr int kQkRow = 576;              // bytes of one node's k (or q): 8 step
 
 template <int NT>
 struct TreeCfg {
+  static_assert(NT == 1 || NT == 2 || NT == 4, "up to 32 nodes");
   static constexpr int TP = 8 * NT;                       // nodes, padded
   static constexpr int KT = (TP + 15) / 16;               // 16-node blocks
   static constexpr int kSolvers = NT <= 2 ? 1 : 2;
@@ -269,39 +270,33 @@ __global__ void __launch_bounds__(TreeCfg<NT>::kThreads, TreeCfg<NT>::kMinCtas)
         }
       }
       if (C::kSolvers > 1) named_bar_sync(4, kSolve); else __syncwarp();
-      // a lane per (row t, column j): a warp takes 32 / TP rows at a time, or half a row (columns past 31 only where the
-      // row has ancestors there)
-      constexpr int kRowsAtOnce = TP < 32 ? 32 / TP : 1;
+      // a lane per (row t, column j): a warp takes 32 / TP rows at a time
+      constexpr int kRowsAtOnce = 32 / TP;
 #pragma unroll(TP < 32 ? 4 : 2)
       for (int t0 = sw * kRowsAtOnce; t0 < TP; t0 += C::kSolvers * kRowsAtOnce) {
-        const int t = t0 + (TP < 32 ? lane / TP : 0);
+        const int t = t0 + lane / TP, j = lane % TP;
         const unsigned long long mt = tree.mask[t];
-        const float2 gt = sum_s[t];
+        const float2 gt = sum_s[t], gj = sum_s[j];
         const float be = beta_s[jh][t];
-#pragma unroll
-        for (int half = 0; half < (TP > 32 ? 2 : 1); ++half) {
-          if (half == 1 && (mt >> 32) == 0ull) break;
-          const int j = lane % (TP < 32 ? TP : 32) + 32 * half;
-          const float2 gj = sum_s[j];
-          const float kk = kk_s[t * C::MR + j], qk = kk_s[(TP + t) * C::MR + j];
-          const float dec = j == t ? 1.f : __expf((gt.x - gj.x) + (gt.y - gj.y));
-          const float pv = dec * qk;
-          float av = be * dec * kk;
-          if ((mt >> j) & 1) {
-            put(tsm + C::kOffP + img(t, j), pv);
-            if (j < t) {
-              if (!isfinite(av)) {
-                atomicOr(&poison_s[jh], 1ull << t);
-                av = 0.f;
-              }
-              if ((t >> 4) == (j >> 4)) d_s[(t >> 4) * 320 + (t & 15) * 20 + (j & 15)] = av;
-              else put(tsm + C::kOffM + img(t, j), -av);
+        const float kk = kk_s[t * C::MR + j], qk = kk_s[(TP + t) * C::MR + j];
+        const float dec = j == t ? 1.f : __expf((gt.x - gj.x) + (gt.y - gj.y));
+        const float pv = dec * qk;
+        float av = be * dec * kk;
+        if ((mt >> j) & 1) {
+          put(tsm + C::kOffP + img(t, j), pv);
+          if (j < t) {
+            if (!isfinite(av)) {
+              atomicOr(&poison_s[jh], 1ull << t);
+              av = 0.f;
             }
+            if ((t >> 4) == (j >> 4)) d_s[(t >> 4) * 320 + (t & 15) * 20 + (j & 15)] = av;
+            else put(tsm + C::kOffM + img(t, j), -av);
           }
         }
       }
       if (C::kSolvers > 1) named_bar_sync(4, kSolve); else __syncwarp();
       // T_b: a lane per column of a 16 x 16 block, x_t = e_t - sum_{i < t} A_ti x_i down the column in registers
+      // (invert_column written out: as a call it spills more registers at NT = 2, 64 sequences x 16 nodes 84 -> 88 us)
       if (sw * 2 < KT) {
         const int b = 2 * sw + (lane >> 4), col = lane & 15;
         if (b < KT && 16 * b + col < TP) {

@@ -1,4 +1,5 @@
-// What the two kernels of gdn_decode_tree share (gdn_tree.cu up to 32 nodes, gdn_tree_wide.cu beyond).
+// What the three kernels of gdn_decode_tree share (gdn_tree.cu up to 32 nodes, gdn_tree_small.cu up to 8 with several value heads
+// per CTA, gdn_tree_wide.cu beyond 32).
 #pragma once
 
 #include "gdn_tree.cuh"
