@@ -9,7 +9,7 @@ import torch
 import oracle
 from gated_delta_rule_81_b200 import gdn
 from gpu_helpers import OUT_TOL, out_error
-from test_gpu_tree import KEYS, attn_case, attn_run, delta_case, delta_ref
+from test_gpu_tree import KEYS, attn_case, attn_run, delta_case, delta_ref, dev_tree, make_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -75,6 +75,32 @@ def test_attention_tree_key_that_is_not_finite_reaches_its_descendants(value, le
                                      lens[:1], c["rows"][:1], c["g"][:T].cpu())["out"]
     want = torch.from_numpy(np.isnan(ref)).cuda()
     assert torch.equal(torch.isnan(out[0])[hit[0]], want[hit[0]])
+
+
+@pytest.mark.parametrize("lens", [[500], [300] * 150])
+def test_attention_tree_whole_tiles_of_lowest_values_and_masked_infinite_scores(lens):
+    """Two whole tiles of keys whose scores are about -2e36 before any others, and nodes off the path with infinite scores of both
+    signs: each row's weights are those of the keys that it sees.  (A score is a power of two times whole numbers below 2^8
+    here, so sums are exact, whatever their order.)"""
+    N, T, H, D = len(lens), 6, 4, 128
+    c = attn_case(N, T, H, 4, D, lens, "flat", seed=4, gate=False)
+    low = -2.0 ** 117  # 128 of them: -2^124 / 128 ** 0.5 = about -1.9e36 each score
+    c["q"].fill_(1.0)
+    c["kc"][:, :256] = low
+    c["kc"][:, 256:] = 0.0
+    c["kt"].zero_()
+    c["kt"].view(N, T, 4, D)[:, 1] = float("inf")
+    c["kt"].view(N, T, 4, D)[:, 4] = -float("inf")
+    out = attn_run(c).view(N, T, H, D)
+    assert bool(torch.isnan(out[:, 1]).all()) and bool(torch.isfinite(out[:, [0, 2, 3, 5]]).all())
+    for n in range(min(N, 3)):
+        old = c["vc"][n, 256:lens[n]].double()
+        for t in (0, 2, 3, 4, 5):  # uniform weights over the zero scores; node 4's own score weighs nothing
+            seen = old if t == 4 else torch.cat([old, c["vt"].view(N, T, 4, D)[n, t].double()[None]])
+            want = seen.mean(0)
+            # the weights are exactly 1 in bf16, so what is left is the sums' (len 2^-24 of sum |v| each) and the output's rounding
+            tol = 2.0 ** -8 * want.abs() + 2 * len(seen) * 2.0 ** -24 * seen.abs().mean(0)
+            assert bool(((out[n, t].double() - want).abs() <= tol).all())
 
 
 # ------------------------------------------------------------------ gdn_qk_norm_rope
@@ -267,3 +293,64 @@ def test_attention_tree_of_no_sequences():
         out = gdn.attention_tree(e(0, 4, 128), e(0, 2, 128), e(0, 2, 128), e(0, 9, 2, 128), e(0, 9, 2, 128),
                                  torch.empty(0, dtype=torch.int32, device="cuda"), parent)
         assert out.shape == (0, 512)
+
+
+# ------------------------------------------------------------------ layers
+
+@pytest.mark.parametrize("N,T", [(1, 1), (1, 3), (2, 11), (3, 40), (160, 5)])
+def test_layer_tree_calls_are_their_parts(N, T):
+    """Both layers' tree calls: bitwise the projection, the direct calls on its columns and the other projection; the commits
+    those of the direct calls on what the workspace keeps."""
+    g = torch.Generator().manual_seed(N + T)
+    hidden, H_k, H_v, cap = 192, 2, 6, 90
+
+    def mat(r, c):
+        return (torch.randn(r, c, generator=g) * c ** -0.5).to(torch.bfloat16).cuda()
+
+    rows = make_tree("holes", N, T, seed=N)
+    parent = dev_tree(rows)
+    ps = [oracle.tree.paths(r) for r in rows]
+    acc = torch.tensor([max((t for t in range(T) if p[t]), key=lambda t: len(p[t])) for p in ps], dtype=torch.int32, device="cuda")
+    x = torch.randn(N * T, hidden, generator=g).to(torch.bfloat16).cuda()
+    # the delta-rule layer
+    n_in = int(gdn.load().gdn_layer_n_in(H_k, H_v))
+    w_in, w_out = mat(n_in, hidden), mat(hidden, H_v * 128)
+    conv_w = (torch.randn((2 * H_k + H_v) * 128, 4, generator=g) * 0.5).to(torch.bfloat16).cuda()
+    A_log = (torch.rand(H_v, generator=g) * 2).cuda()
+    norm_w = (1 + 0.1 * torch.randn(128, generator=g)).to(torch.bfloat16).cuda()
+    L = gdn.make_layer(w_in, w_out, conv_w, A_log, norm_w, H_k, H_v, scale=0.7)
+    S = (torch.randn(N, H_v, 128, 128, generator=g) * 0.1).cuda()
+    C = torch.randn(N, 3, (2 * H_k + H_v) * 128, generator=g).to(torch.bfloat16).cuda()
+    ws = gdn.layer_tree_workspace(L, N, T, "cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = gdn.layer_decode_tree(L, N, T, parent, x, S, C, ws, err=err)
+    proj = torch.empty(N * T, -(-n_in // 8) * 8, dtype=torch.bfloat16, device="cuda")
+    gdn.gemm_bf16(x, w_in, out=proj[:, :n_in])
+    q, k, v, z, a, b = proj[:, :n_in].split([H_k * 128, H_k * 128, H_v * 128, H_v * 128, H_v, H_v], 1)
+    s = gdn.make_inputs(q, k, v, a, b, z, conv_w, A_log, norm_w, scale=0.7)
+    assert torch.equal(gdn.gemm_bf16(gdn.decode_tree(s, N, T, parent, S, C).view(N * T, -1), w_out), y)
+    S2, C2 = gdn.decode_tree_commit(s, N, T, parent, acc, S, C, state_out=torch.empty_like(S), conv_out=torch.empty_like(C))
+    gdn.layer_tree_commit(L, N, T, parent, acc, S, C, ws, err=err)
+    assert torch.equal(S, S2) and torch.equal(C, C2)
+    # the attention layer, on the other's output
+    w_in, w_out = mat(gdn.ATTN_N_IN, hidden), mat(hidden, 24 * 256)
+    nq, nk = ((1 + 0.1 * torch.randn(256, generator=g)).to(torch.bfloat16).cuda() for _ in range(2))
+    L = gdn.make_attn_layer(w_in, w_out, nq, nk)
+    kc, vc = (torch.randn(N, cap, 4, 256, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    lens = torch.tensor([(n * 7) % (cap - T + 1) for n in range(N)], dtype=torch.int32, device="cuda")
+    ws = gdn.attn_layer_tree_workspace(N, T, "cuda")
+    x = y
+    y = gdn.attn_layer_decode_tree(L, N, T, parent, x, kc, vc, lens, ws, err=err)
+    q, gate, k, v = gdn.gemm_bf16(x, w_in).split([24 * 256, 24 * 256, 4 * 256, 4 * 256], 1)
+    heads = lambda t: t.unflatten(1, (-1, 256))
+    depth = torch.tensor([[max(len(p) - 1, 0) for p in tree] for tree in ps], dtype=torch.int32, device="cuda")
+    pos = (lens[:, None] + depth).reshape(-1)
+    q, k, _ = gdn.qk_norm_rope(gdn.make_rope(256, 64), heads(q), heads(k), q_norm_w=nq, k_norm_w=nk, positions=pos)
+    there = torch.tensor([bool(p) for tree in ps for p in tree], device="cuda")
+    out = gdn.attention_tree(q, k, heads(v), kc, vc, lens, parent, g=heads(gate))
+    assert torch.equal(gdn.gemm_bf16(out, w_out), y) and bool((y[~there] == 0).all())
+    kc2, vc2, lens2 = kc.clone(), vc.clone(), lens.clone()
+    gdn.attn_tree_commit(k, heads(v), T, parent, acc, kc2, vc2, lens2)
+    gdn.attn_layer_tree_commit(N, T, parent, acc, kc, vc, lens, ws, err=err)
+    assert torch.equal(kc, kc2) and torch.equal(vc, vc2) and torch.equal(lens, lens2)
+    assert int(err.item()) == 0
