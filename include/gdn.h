@@ -436,7 +436,8 @@ gdn_status gdn_decode_tree_commit(const gdn_inputs* in, int N, int T, const int*
  * gdn_decode_tree between the layer's projections, as gdn_layer_decode: x bf16 [N*T][ldx] ->
  * y bf16 [N*T][ldy].  The workspace keeps the projected inputs: pass it, unchanged, to
  * gdn_layer_tree_commit, which advances state and conv_state in place along the accepted paths
- * (one workspace per layer between the step and its commit).  y must not overlap the workspace, the
+ * (one workspace per layer between the step and its commit).  state_slot NULL: sequence n uses slot n of
+ * pools that hold at least N, and n_slots is ignored.  y must not overlap the workspace, the
  * state or the conv state.  L->events, when set, gets 4 records as in gdn_layer_prefill (the commit: none).
  */
 size_t gdn_layer_tree_workspace_size(int H_k, int H_v, int N, int T);
@@ -516,7 +517,8 @@ gdn_status gdn_qk_norm_rope(const gdn_rope* rope, long long n_tok, int H_q, int 
  * What rows beyond cache_len, absent nodes and nodes off a node's path hold (infinities and NaN
  * included) does not reach its output.  head_dim is 128 or 256 and H_q / H_kv at most 16 (else
  * GDN_ERR_UNSUPPORTED); scale > 0 and finite.  The probabilities enter the tensor cores as bf16 (relative error
- * <= 2^-9 each), sums and statistics are fp32.  Repeated calls give bitwise equal results.
+ * <= 2^-8 each, as in gdn_attention_prefill; gdn_attn_layer_decode_step takes pairs hi + lo), sums and statistics
+ * are fp32.  A row that sees a score of NaN, +inf, or nothing but -inf is NaN.  Repeated calls give bitwise equal results.
  *   workspace  device scratch of gdn_attention_tree_workspace_size bytes, 16-byte aligned, not shared
  *              with a call that may run at the same time; contents need no initialisation
  */

@@ -87,6 +87,17 @@ def test_header_says_what_the_commit_reads():
     assert "last raw rows of q, k and v become the conv state" in doc
 
 
+def test_header_bounds_a_bf16_rounding():
+    """A rounding to bf16 is off by up to 2^-8 of the value, not 2^-9: the header's bound for attention's probabilities."""
+    x = torch.linspace(1, 2, 100001, dtype=torch.float64)
+    off = float(((x.to(torch.bfloat16).double() - x).abs() / x).max())
+    assert 2.0 ** -9 < off <= 2.0 ** -8
+    with open(os.path.join(build.INCLUDE, "gdn.h")) as f:
+        text = " ".join(f.read().replace("*", " ").split())
+    doc = text[text.index("Attention of a tree's nodes over a KV cache"):text.index("size_t gdn_attention_tree_workspace_size(")]
+    assert "2^-9" not in doc and "(relative error <= 2^-8 each" in doc
+
+
 def attention(lib, H=24, Hkv=4, D=256, scale=0.0625, N=2, T=4, cap=100, ld_q=None, ld_kt=None, out=OUT, ws=7 << 36, nb=None,
               k=8 << 36, v=9 << 36, g=None, ld_g=0, q=10 << 36, ln=11 << 36):
     nb = lib.gdn_attention_tree_workspace_size(H, Hkv, D, N, T) if nb is None else nb
