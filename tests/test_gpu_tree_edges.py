@@ -9,7 +9,7 @@ import torch
 import oracle
 from gated_delta_rule_81_b200 import gdn
 from gpu_helpers import OUT_TOL, out_error
-from test_gpu_tree import KEYS, attn_case, attn_run, delta_case, delta_ref, dev_tree, make_tree
+from test_gpu_tree import KEYS, attn_case, attn_check, attn_run, delta_case, delta_ref, dev_tree, make_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -103,6 +103,15 @@ def test_attention_tree_whole_tiles_of_lowest_values_and_masked_infinite_scores(
             assert bool(((out[n, t].double() - want).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("N,T,H,Hkv,D,lens", [(1, 64, 16, 1, 256, [700]), (3, 50, 48, 3, 128, [129, 0, 640]), (2, 3, 64, 64, 128, [257, 30])])
+def test_attention_tree_most_heads_of_each_kind(N, T, H, Hkv, D, lens):
+    """16 query heads to a KV head at both head sizes, and as many KV heads as query heads."""
+    c = attn_case(N, T, H, Hkv, D, lens, "holes", seed=N * T)
+    out = attn_run(c)
+    attn_check(c, out)
+    assert torch.equal(attn_run(c), out)
+
+
 # ------------------------------------------------------------------ gdn_qk_norm_rope
 
 def test_rope_amplitude_of_the_caller():
@@ -152,6 +161,16 @@ def test_decode_tree_gate_that_forgets_everything(N, T, H_k, H_v, value):
     ref = oracle.tree.mixer_tree(sub["inp"], sub["rows"], c["state"][sl], c["conv"][sl])["out"]
     assert np.isfinite(ref).all()
     assert out_error(out[:n * T], ref) <= OUT_TOL
+
+
+@pytest.mark.parametrize("T", [1, 5, 8])
+@pytest.mark.parametrize("N", [1, 70])
+def test_decode_tree_as_many_value_heads_as_key_heads(N, T):
+    c = delta_case(N, T, 3, 3, "holes", seed=N + T)
+    out = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"])
+    t = c["there"].numpy()
+    assert bool((out[~c["there"].cuda()] == 0).all())
+    assert out_error(out[c["there"].cuda()], delta_ref(c)["out"][t]) <= OUT_TOL
 
 
 # ------------------------------------------------------------------ gdn_decode_tree_commit
