@@ -173,6 +173,38 @@ def test_decode_tree_as_many_value_heads_as_key_heads(N, T):
     assert out_error(out[c["there"].cuda()], delta_ref(c)["out"][t]) <= OUT_TOL
 
 
+@pytest.mark.parametrize("N,T", [(3, 5), (160, 5), (3, 16), (3, 30), (3, 60), (160, 60)])
+def test_a_sequence_without_nodes(N, T):
+    """A padded batch: one sequence has no node at all.  Zero rows for it, through both mixers, the others as they were; its
+    commits accept nothing, and a node accepted all the same is reported."""
+    c = delta_case(N, T, 1, 3, "chain", seed=T)
+    want = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"]).view(N, T, -1)
+    c["parent"][1] = -2
+    for k in KEYS:
+        c["dev"][k][T:2 * T] = float("nan")
+    out = gdn.decode_tree(c["s"], N, T, c["parent"], c["d_state"], c["d_conv"], state_slot=c["d_slot"]).view(N, T, -1)
+    others = torch.arange(N, device="cuda") != 1
+    assert bool((out[1] == 0).all()) and torch.equal(out[others], want[others])
+    a = attn_case(N, T, 8, 2, 128, [(n * 31) % 200 for n in range(N)], "chain", seed=T)
+    want = attn_run(a).view(N, T, -1)
+    a["parent"][1] = -2
+    a["q"].view(N, T, 8, 128)[1] = float("nan")
+    out = attn_run(a).view(N, T, -1)
+    assert bool((out[1] == 0).all()) and torch.equal(out[others], want[others])
+    for last, bits in ((-1, 0), (0, 128)):
+        acc = torch.full((N,), last, dtype=torch.int32, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        S, C = c["d_state"].clone(), c["d_conv"].clone()
+        gdn.decode_tree_commit(c["s"], N, T, c["parent"], acc, S, C, state_slot=c["d_slot"], err=err)
+        slot = int(c["slot"][1])
+        assert torch.equal(S[slot], c["d_state"][slot]) and torch.equal(C[slot], c["d_conv"][slot]) and bool(torch.isfinite(S).all())
+        assert int(err.item()) == bits
+        err.zero_()
+        kc, vc = torch.zeros(N, 210, 2, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(N, 210, 2, 128, dtype=torch.bfloat16, device="cuda")
+        new = gdn.attn_tree_commit(a["kt"], a["vt"], T, a["parent"], acc, kc, vc, a["len"], cache_len_out=torch.empty_like(a["len"]), err=err)
+        assert torch.equal(new, a["len"] + (last + 1) * others.int()) and not bool(kc[1].any()) and int(err.item()) == bits
+
+
 # ------------------------------------------------------------------ gdn_decode_tree_commit
 
 def test_decode_tree_commit_reads_the_path_s_query_rows():
