@@ -24,10 +24,14 @@
 // S -> softmax -> P V round trip is paid twice as often.  The next unit's Q is fetched and its first S issued while
 // this one's epilogue runs.
 //
-// Measured (B200, 24 / 4 heads of 256, kernels alone): one sequence of 262,144 keys x 64 nodes 380 - 388 us, 1.07 PFLOP/s, bound by
-// shared memory (a tile's 64 KB of Q, 64 + 64 KB of K and V read and 128 KB written take 2500 of its 3200 cycles, the products
-// 2050); 64 ragged sequences of up to 8192 keys x 16 nodes 226 us (5510 GB/s over all, HBM's rate while tiles stream), x 1 node 197
-// us (6140 GB/s); one token of 777 keys 14 us.
+// Measured (B200, 24 / 4 heads of 256, in a graph): one sequence of 262,144 keys x 64 nodes 368 - 372 us after a pause (1.12
+// PFLOP/s), 380 - 428 us in a long run, when the power cap holds the SM clock at 1.46 GHz; of a tile's 3200 cycles shared memory takes 2500 (64
+// KB of Q, 64 + 64 KB of K and V read and 128 KB written), the products 2050, the rest is not explained.  64 ragged sequences of up to 8192
+// keys x 16 nodes 230 us (5.4 TB/s over all, HBM's rate while tiles stream; 249 us in a long run at 1.43 GHz), x 1 node 197 us (6140
+// GB/s); one token of 777 keys 15 us.
+//
+// P enters the products as bf16, within 2^-8, like the prefill attention's: a pair hi + lo would double the P V products, and the
+// error against 64 bits (0.0023 of the output, 0.0017 of it the output's own rounding) does not call for it.
 //
 // Whatever a row may not see contributes exactly nothing: masked scores become -inf by selection, so infinities
 // and NaN in masked keys vanish; masked values meet a zero probability in the product, so the

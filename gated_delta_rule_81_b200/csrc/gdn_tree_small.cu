@@ -5,8 +5,8 @@
 // first, a warp per head, and then each warp runs its 16 state rows of one head after the other (v, X, U, O) without meeting the others
 // until the norm at the end.  Eight warps of 64 registers, four CTAs per SM.
 //
-// Measured (B200, 16 / 48 heads): 256 sequences x 8 nodes 180 us (5.0 TB/s of the 906 MB it cannot do without; the kernel of gdn_tree.cu
-// 194), 256 x 1 152 us (172), 64 x 8 52 us (57).  Bringing the state into L2 ahead of the loads changed nothing at one
+// Measured (B200, 16 / 48 heads, in a graph): 256 sequences x 8 nodes 180 - 189 us (5.0 TB/s of the 906 MB it cannot do without; the
+// kernel of gdn_tree.cu 194), 256 x 1 152 us (172), 64 x 8 52 us (57).  Bringing the state into L2 ahead of the loads changed nothing at one
 // head ahead and cost 10% at all heads; templates of 16 nodes this way took 99 against 75 us at 64 x 16.
 #include "gdn_tree_delta.cuh"
 
